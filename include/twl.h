@@ -306,6 +306,40 @@ twl_status twl_rotate_quant_linear(const uint16_t* x, const int8_t* sign, const 
  */
 int twl_rotate_quant_linear_fused(int64_t M, int64_t N, int64_t K);
 
+/*
+ * norm_rotate_quant_act -- the step between two blocks, fused with the next
+ * projection's input: norm after the block, gate, residual scale and residual
+ * add, norm before the next block, rotate_quant_act.  The pages name neither
+ * the model's norms nor its residual path; RMSNorm and the order below are this
+ * library's reading.  Per token, in fp64 up to the two bf16 roundings:
+ *   b = x
+ *   b = b / sqrt(mean_k(b^2) + eps) * post_weight     if post_weight
+ *   b = b * gate                                      if gate
+ *   b = b * branch_scale
+ *   h = bf16(residual + b)      (no residual: bf16(b))
+ *   n = bf16(h / sqrt(mean_k(h^2) + eps) * weight)
+ *   x_i8, a_scale = rotate_quant_act(n, sign)          (bit for bit)
+ * With none of residual, post_weight, gate and branch_scale != 1, h is x.
+ *   x           in : bf16 bit patterns [M, K], the block's output
+ *   residual    in : bf16 [M, K], or NULL
+ *   post_weight in : bf16 [K], or NULL
+ *   gate        in : bf16, row t at gate + t * gate_stride elements (0: one row
+ *                    [K] for all tokens; else a multiple of 8, at least K), or NULL
+ *   weight      in : bf16 [K];  sign in: int8 +-1 [K], or NULL: no rotation
+ *   h           out: bf16 [M, K], or NULL; may be x or residual themselves
+ *   normed      out: n as bf16 [M, K], or NULL (required when sign is NULL)
+ *   x_i8        out: int8 [M, K];  a_scale out: fp32 [M]  (NULL when sign is)
+ * eps must be positive.  Outputs that overlap an input (other than h) or each
+ * other are TWL_EINVAL.  A row whose values are not finite gives unspecified
+ * results in that row only.
+ */
+twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual,
+                                     const uint16_t* post_weight, const uint16_t* gate,
+                                     int64_t gate_stride, double branch_scale,
+                                     const uint16_t* weight, double eps, const int8_t* sign,
+                                     int64_t M, int64_t K, uint16_t* h, uint16_t* normed,
+                                     int8_t* x_i8, float* a_scale, hipStream_t stream);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* twl_last_error(void);
 

@@ -1,0 +1,32 @@
+"""CPU oracle of the block operators around the ternary linear layer: the
+definitions of include/twl.h in float64 NumPy, written without the kernels'
+splits and layouts."""
+import numpy as np
+
+from .twl_oracle import bf16_to_f32, round_bf16, rotate_quant_act
+
+
+def bf16_bits(v: np.ndarray) -> np.ndarray:
+    """float64 -> bf16 bit patterns (through float32, nearest even)."""
+    return round_bf16(np.asarray(v).astype(np.float32))
+
+
+def _rms(t, w_bits, eps):
+    return t / np.sqrt(np.mean(t * t, axis=1, keepdims=True) + eps) * bf16_to_f32(w_bits).astype(np.float64)
+
+
+def norm_rotate_quant_act(x_bits, weight_bits, sign, eps, residual_bits=None, post_bits=None, gate_bits=None,
+                          branch_scale=1.0):
+    """-> (x_i8, a_scale, h bits, normed bits)."""
+    b = bf16_to_f32(x_bits).astype(np.float64)
+    if post_bits is not None:
+        b = _rms(b, post_bits, eps)
+    if gate_bits is not None:
+        b = b * bf16_to_f32(gate_bits).astype(np.float64)
+    b = b * branch_scale
+    if residual_bits is not None:
+        b = bf16_to_f32(residual_bits).astype(np.float64) + b
+    h = bf16_bits(b)
+    normed = bf16_bits(_rms(bf16_to_f32(h).astype(np.float64), weight_bits, eps))
+    x_i8, a_scale = rotate_quant_act(normed, sign) if sign is not None else (None, None)
+    return x_i8, a_scale, h, normed

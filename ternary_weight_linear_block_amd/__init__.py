@@ -7,6 +7,9 @@ Three operations, each one call into the C ABI declared in include/twl.h
   pack_ternary(code, s)                  -> (packed, q, smax)
   ternary_linear(x_i8, a_scale, packed, q, smax) -> y
 
+The operators of the block around them are in block.py: norm_rotate_quant_act
+(norms, gate, residual and the rotation in one pass).
+
 PyTorch provides device memory and the current stream.  Tensors must be CUDA
 (HIP) tensors on the current device, contiguous; x is bf16 (or its int16 bit
 pattern), s is fp16 (or int16 bits), code and sign are int8.
@@ -26,6 +29,7 @@ __all__ = [
     "workspace_bytes", "packed_bytes", "plan_info", "TwlError", "PATH_AUTO", "PATH_GEMM", "PATH_GEMV", "PATH_GEMV_DOT4",
     "PATH_GEMV_MFMA", "GEMV_MAX_M",
     "HBLOCK", "GROUP", "MAX_K", "library",
+    "norm_rotate_quant_act",
 ]
 
 
@@ -329,3 +333,7 @@ def ternary_linear_acc(x_i8, packed, q, path: int = PATH_AUTO, out=None, workspa
                        stream=None):
     """The exact int32 accumulators acc [M, N] of the same kernels (no rescale)."""
     return _linear(x_i8, None, packed, q, None, _lib.OUT_ACC_I32, path, out, workspace, stream)
+
+
+# the block operators around the linear layer
+from .block import norm_rotate_quant_act  # noqa: E402

@@ -24,6 +24,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SIZE = ctypes.c_size_t
 _INT = ctypes.c_int
+_F64 = ctypes.c_double
 SIGNATURES = [
     ("twl_rotate_quant_act", _INT, [_P, _P, _I64, _I64, _P, _P, _P]),
     ("twl_silu_mul_rotate_quant_act", _INT, [_P, _P, _I64, _I64, _P, _P, _P]),
@@ -42,6 +43,8 @@ SIGNATURES = [
     ("twl_rotate_quant_linear", _INT,
      [_P, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _P, _P, _INT, _P, _SIZE, _P]),
     ("twl_rotate_quant_linear_fused", _INT, [_I64, _I64, _I64]),
+    ("twl_norm_rotate_quant_act", _INT,
+     [_P, _P, _P, _P, _I64, _F64, _P, _F64, _P, _I64, _I64, _P, _P, _P, _P, _P]),
     ("twl_last_error", ctypes.c_char_p, []),
     ("twl_abi_version", _INT, []),
 ]

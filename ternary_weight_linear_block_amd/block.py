@@ -1,0 +1,107 @@
+"""The operators of the block around the ternary linear layer: Python binding of
+their entry points in include/twl.h (argument checks and marshalling only).
+
+Tensors must be contiguous CUDA (HIP) tensors on the current device; bf16
+arguments may also be given as their int16 bit patterns.  Outputs and workspaces
+that a call allocates belong to the stream the call runs on.
+"""
+from __future__ import annotations
+
+import contextlib
+
+from . import _lib
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _check(t, name, shape, dtypes):
+    """The device pointer of a tensor argument of this shape."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _matrix(t, name):
+    """The sizes of a two-dimensional tensor argument."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected two dimensions")
+    return t.shape
+
+
+def _on(stream):
+    """Context in which allocations belong to the stream of the call, and its handle."""
+    torch = _torch()
+    if stream is None:
+        return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
+    if stream.device.index != torch.cuda.current_device():
+        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def norm_rotate_quant_act(x, weight, sign, eps=1e-6, residual=None, post_weight=None, gate=None,
+                          branch_scale=1.0, return_normed=False, x_i8=None, a_scale=None, h=None,
+                          normed=None, stream=None):
+    """The step between two blocks (twl_norm_rotate_quant_act): RMSNorm of the
+    block's output x with post_weight, times gate ([K] or [M, K]) and
+    branch_scale, plus residual -> h; RMSNorm of h with weight -> normed;
+    rotate_quant_act(normed, sign).
+
+    x and residual [M, K] bf16, weights [K] bf16, sign [K] int8 (None: no
+    rotation).  Returns (x_i8, a_scale, h, normed): h is None when nothing
+    changes x (no residual, post_weight, gate or branch_scale), normed unless
+    return_normed, x_i8 and a_scale without sign.  Buffers given for the outputs
+    are written and returned; h may be x or residual itself.  return_normed, or
+    normed=, is required without sign."""
+    torch = _torch()
+    lib = _lib.load()
+    M, K = _matrix(x, "x")
+    bf16 = (torch.bfloat16, torch.int16)
+    branch = residual is not None or post_weight is not None or gate is not None or branch_scale != 1.0
+    ctx, handle = _on(stream)
+    gate_stride = 0
+    p = {"x": _check(x, "x", (M, K), bf16), "weight": _check(weight, "weight", (K,), bf16)}
+    for name, t, shape, dtypes in (("residual", residual, (M, K), bf16), ("post_weight", post_weight, (K,), bf16),
+                                   ("sign", sign, (K,), (torch.int8,))):
+        p[name] = None if t is None else _check(t, name, shape, dtypes)
+    p["gate"] = None
+    if gate is not None:
+        wide = isinstance(gate, torch.Tensor) and gate.dim() == 2
+        p["gate"] = _check(gate, "gate", (M, K) if wide else (K,), bf16)
+        gate_stride = K if wide else 0
+    if sign is None and (x_i8 is not None or a_scale is not None):
+        raise ValueError("x_i8 and a_scale need sign")
+    if h is not None and not branch:
+        raise ValueError("h is given, but no residual, post_weight, gate or branch_scale: it would be x")
+    with ctx:
+        if sign is not None and x_i8 is None:
+            x_i8 = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        if sign is not None and a_scale is None:
+            a_scale = torch.empty((M,), dtype=torch.float32, device=x.device)
+        if branch and h is None:
+            h = torch.empty((M, K), dtype=x.dtype, device=x.device)
+        if return_normed and normed is None:
+            normed = torch.empty((M, K), dtype=x.dtype, device=x.device)
+    for name, t, shape, dtypes in (("h", h, (M, K), bf16), ("normed", normed, (M, K), bf16),
+                                   ("x_i8", x_i8, (M, K), (torch.int8,)), ("a_scale", a_scale, (M,), (torch.float32,))):
+        p[name] = None if t is None else _check(t, name, shape, dtypes)
+    st = lib.twl_norm_rotate_quant_act(
+        p["x"], p["residual"], p["post_weight"], p["gate"], gate_stride, branch_scale, p["weight"], eps,
+        p["sign"], M, K, p["h"], p["normed"], p["x_i8"], p["a_scale"], handle)
+    _lib.check(st, "twl_norm_rotate_quant_act")
+    return x_i8, a_scale, h, normed

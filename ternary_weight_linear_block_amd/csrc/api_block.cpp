@@ -1,0 +1,104 @@
+// C ABI of the block operators around the ternary linear layer (include/twl.h):
+// argument validation and launches.  The same rules as api.cpp: nothing is
+// allocated, nothing synchronises, every kernel goes to the caller's stream.
+#include "api_common.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace {
+
+using namespace twl::api;
+
+// A byte range an argument covers; empty for a null pointer.
+struct Range {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+
+bool overlap(const Range& a, const Range& b) {
+  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
+  const auto pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  return pa < pb + b.bytes && pb < pa + a.bytes;
+}
+
+// As TWL_REQUIRE_PTR for an argument that may be NULL.
+#define TWL_OPTIONAL_PTR(p)                                                                     \
+  do {                                                                                          \
+    if (!aligned16(p)) return fail(TWL_EALIGN, "%s is not 16-byte aligned", #p);                \
+  } while (0)
+
+}  // namespace
+
+extern "C" {
+
+twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual,
+                                     const uint16_t* post_weight, const uint16_t* gate,
+                                     int64_t gate_stride, double branch_scale,
+                                     const uint16_t* weight, double eps, const int8_t* sign,
+                                     int64_t M, int64_t K, uint16_t* h, uint16_t* normed,
+                                     int8_t* x_i8, float* a_scale, hipStream_t stream) {
+  TWL_TRY(check_rows("M", M));
+  TWL_TRY(check_k(K));
+  if (!(eps > 0.0) || !std::isfinite(eps)) return fail(TWL_EINVAL, "eps=%g must be positive and finite", eps);
+  if (!std::isfinite(branch_scale)) return fail(TWL_EINVAL, "branch_scale=%g must be finite", branch_scale);
+  if (gate_stride != 0 && (gate_stride < K || gate_stride % 8 != 0 || gate_stride > (int64_t{1} << 40)))
+    return fail(TWL_ESHAPE, "gate_stride=%lld must be 0 or a multiple of 8 of at least K=%lld",
+                static_cast<long long>(gate_stride), static_cast<long long>(K));
+  const bool branch = residual != nullptr || post_weight != nullptr || gate != nullptr || branch_scale != 1.0;
+  if (h != nullptr && !branch)
+    return fail(TWL_EINVAL, "h is given, but no residual, post_weight, gate or branch_scale: it would be x");
+  if (sign == nullptr) {
+    if (x_i8 != nullptr || a_scale != nullptr) return fail(TWL_EINVAL, "x_i8 and a_scale need sign");
+    if (M > 0 && normed == nullptr) return fail(TWL_EINVAL, "sign and normed are both NULL: no output");
+  }
+  if (M == 0) return ok();
+  TWL_REQUIRE_PTR(x);
+  TWL_REQUIRE_PTR(weight);
+  TWL_OPTIONAL_PTR(residual);
+  TWL_OPTIONAL_PTR(post_weight);
+  TWL_OPTIONAL_PTR(gate);
+  TWL_OPTIONAL_PTR(h);
+  TWL_OPTIONAL_PTR(normed);
+  if (sign != nullptr) {
+    TWL_REQUIRE_PTR(sign);
+    TWL_REQUIRE_PTR(x_i8);
+    TWL_REQUIRE_PTR(a_scale);
+  }
+  // outputs may not overlap anything but h its own x or residual, element for
+  // element (each lane reads what it overwrites first)
+  const size_t rows = static_cast<size_t>(M), wide = rows * K * 2, table = static_cast<size_t>(K) * 2;
+  const size_t gate_bytes = table + (rows - 1) * static_cast<size_t>(gate_stride) * 2;
+  const Range out[] = {{h, wide, "h"}, {normed, wide, "normed"}, {x_i8, rows * K, "x_i8"}, {a_scale, rows * 4, "a_scale"}};
+  const Range in[] = {{x, wide, "x"}, {residual, wide, "residual"}, {post_weight, table, "post_weight"},
+                      {gate, gate_bytes, "gate"}, {weight, table, "weight"}, {sign, static_cast<size_t>(K), "sign"}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 6; ++j)
+      if (overlap(out[i], in[j]) && !(i == 0 && j < 2 && out[i].p == in[j].p))
+        return fail(TWL_EINVAL, "%s overlaps %s", out[i].name, in[j].name);
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return fail(TWL_EINVAL, "%s overlaps %s", out[i].name, out[j].name);
+  }
+  twl::DeviceInfo dev;
+  TWL_TRY(current_device(&dev));
+  twl::NormArgs a = {};
+  a.x = x;
+  a.residual = residual;
+  a.post_weight = post_weight;
+  a.gate = gate;
+  a.weight = weight;
+  a.sign = sign;
+  a.h = h;
+  a.normed = normed;
+  a.x_i8 = x_i8;
+  a.a_scale = a_scale;
+  a.branch_scale = branch_scale;
+  a.eps = eps;
+  a.M = M;
+  a.gate_stride = gate_stride;
+  a.K = static_cast<int>(K);
+  return launched(twl::launch_norm_rotate(a, stream), "norm_rotate_quant_act");
+}
+
+}  // extern "C"

@@ -82,4 +82,25 @@ hipError_t launch_gemv_rot(const uint16_t* x, const int8_t* sign, bool silu, con
                            void* out, OutKind out_kind, int8_t* x_i8, float* a_scale,
                            const DeviceInfo& dev, hipStream_t stream);
 
+// norm_rotate_quant_act (include/twl.h): every pointer but x and weight may be
+// null; sign null leaves out the rotation (x_i8 and a_scale are then not
+// written).  gate_stride: elements between the gate rows of two tokens (0: one
+// row for all).
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* residual;
+  const uint16_t* post_weight;
+  const uint16_t* gate;
+  const uint16_t* weight;
+  const int8_t* sign;
+  uint16_t* h;
+  uint16_t* normed;
+  int8_t* x_i8;
+  float* a_scale;
+  double branch_scale, eps;
+  int64_t M, gate_stride;
+  int K;
+};
+hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t stream);
+
 }  // namespace twl

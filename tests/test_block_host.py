@@ -1,0 +1,78 @@
+"""Host-side checks of the block operators' entry points that need no GPU: bad
+arguments are refused before the device is touched, with the message naming
+the argument, and empty calls enqueue nothing."""
+import os
+
+import pytest
+
+twl = pytest.importorskip("ternary_weight_linear_block_amd")
+from ternary_weight_linear_block_amd import _lib  # noqa: E402
+
+EINVAL, ESHAPE, EALIGN = 1, 2, 3
+# 16-byte aligned addresses far apart, never dereferenced: every call below
+# fails host validation or reaches the device query, which this host fails
+P = [0x10000000 * (i + 1) for i in range(12)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.fail("libtwl.so is not built; run `python -m ternary_weight_linear_block_amd.build`")
+    return _lib.load()
+
+
+def _norm(lib, **kw):
+    a = dict(x=P[0], residual=P[1], post_weight=P[2], gate=P[3], gate_stride=0, branch_scale=1.0, weight=P[4], eps=1e-6,
+             sign=P[5], M=4, K=1024, h=P[6], normed=P[7], x_i8=P[8], a_scale=P[9], stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return lib.twl_norm_rotate_quant_act(*a.values())
+
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(K=1000), ESHAPE, b"K="),
+    (dict(K=65536 + 1024), ESHAPE, b"K="),
+    (dict(M=-1), EINVAL, b"M="),
+    (dict(x=None), EINVAL, b"x is NULL"),
+    (dict(weight=None), EINVAL, b"weight is NULL"),
+    (dict(x_i8=None), EINVAL, b"x_i8 is NULL"),
+    (dict(a_scale=None), EINVAL, b"a_scale is NULL"),
+    (dict(x=P[0] + 8), EALIGN, b"x is not"),
+    (dict(residual=P[1] + 2), EALIGN, b"residual"),
+    (dict(gate=P[3] + 4), EALIGN, b"gate"),
+    (dict(h=P[6] + 2), EALIGN, b"h is not"),
+    (dict(eps=0.0), EINVAL, b"eps"),
+    (dict(eps=float("nan")), EINVAL, b"eps"),
+    (dict(eps=float("inf")), EINVAL, b"eps"),
+    (dict(branch_scale=float("inf")), EINVAL, b"branch_scale"),
+    (dict(gate_stride=1023), ESHAPE, b"gate_stride"),
+    (dict(gate_stride=1028), ESHAPE, b"gate_stride"),
+    (dict(gate_stride=-1024), ESHAPE, b"gate_stride"),
+    (dict(sign=None), EINVAL, b"need sign"),
+    (dict(sign=None, x_i8=None, a_scale=None, normed=None), EINVAL, b"no output"),
+    (dict(residual=None, post_weight=None, gate=None), EINVAL, b"it would be x"),
+    # overlaps: h may be x or residual themselves, not shifted; nothing else may
+    (dict(h=P[0] + 16), EINVAL, b"h overlaps x"),
+    (dict(h=P[3]), EINVAL, b"h overlaps gate"),
+    (dict(normed=P[0]), EINVAL, b"normed overlaps x"),
+    (dict(normed=P[6]), EINVAL, b"normed overlaps h"),
+    (dict(x_i8=P[1]), EINVAL, b"x_i8 overlaps residual"),
+    (dict(a_scale=P[8] + 4096 - 16), EINVAL, b"a_scale overlaps x_i8"),
+])
+def test_norm_refuses(lib, kw, status, word):
+    assert _norm(lib, **kw) == status
+    assert word in lib.twl_last_error()
+
+
+def test_norm_accepts_on_the_host(lib):
+    refused = (EINVAL, ESHAPE, EALIGN)
+    assert _norm(lib) not in refused
+    assert _norm(lib, h=P[0]) not in refused
+    assert _norm(lib, h=P[1]) not in refused
+    assert _norm(lib, h=None, normed=None) not in refused
+    assert _norm(lib, gate_stride=2048) not in refused
+    assert _norm(lib, residual=None, post_weight=None, gate=None, h=None) not in refused
+    assert _norm(lib, sign=None, x_i8=None, a_scale=None) not in refused
+    # the last byte of x_i8 and the first of a_scale next to each other
+    assert _norm(lib, a_scale=P[8] + 4096) not in refused
+    assert _norm(lib, M=0, x=None, weight=None, sign=None, h=None, normed=None, x_i8=None, a_scale=None) == 0

@@ -340,6 +340,38 @@ twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual
                                      int64_t M, int64_t K, uint16_t* h, uint16_t* normed,
                                      int8_t* x_i8, float* a_scale, hipStream_t stream);
 
+/*
+ * lora_add -- low-rank adapters of many requests beside a shared projection:
+ *   v[t,r]   = sum_k x[t,k] A[i,r,k]          with i = ids[t]
+ *   out[t,n] = y[t,n] + scale[i] sum_r v[t,r] B[i,n,r]
+ * A token whose id is outside 0 .. n_adapters-1 (-1, say) has no adapter:
+ * out[t] = y[t].  Sums are fp32; v enters the second product as two bf16 terms
+ * (three for fp32 y), i.e. to 2^-16 (2^-24) of its value; out is rounded once.
+ * Tokens of one adapter need not be adjacent; adjacent ones are faster.
+ *   y     in : [M, N] of the kind (TWL_OUT_F32 or TWL_OUT_BF16)
+ *   x     in : bf16 bit patterns [M, K], the projection's input before rotation
+ *   ids   in : int32 [M]
+ *   lora_a in: bf16 [n_adapters, R, K];  lora_b in: bf16 [n_adapters, N, R]
+ *   scale in : fp32 [n_adapters]
+ *   out   out: [M, N] of the kind; may be y itself (then only rows with an
+ *              adapter are written)
+ *   workspace: twl_lora_workspace_bytes(M, K, R, n_adapters) bytes, contents on
+ *              entry do not matter; calls sharing one must not run concurrently
+ * K a positive multiple of 128 up to TWL_MAX_K; R a multiple of 8 from 8 to
+ * TWL_LORA_MAX_R (pad A and B with zeros for other ranks); N any size; a
+ * kind other than the two, or an output overlapping an input (other than
+ * out == y), is TWL_EINVAL.  n_adapters = 0 copies y.  Values that are not finite
+ * in one adapter or token reach only the tokens that use it.
+ */
+#define TWL_LORA_MAX_R 128
+twl_status twl_lora_add(const void* y, const uint16_t* x, const int32_t* ids, const uint16_t* lora_a,
+                        const uint16_t* lora_b, const float* scale, int64_t M, int64_t N, int64_t K,
+                        int64_t R, int64_t n_adapters, int kind, void* out, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace twl_lora_add needs on the current device (0 for invalid sizes). */
+size_t twl_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t n_adapters);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* twl_last_error(void);
 

@@ -30,3 +30,19 @@ def norm_rotate_quant_act(x_bits, weight_bits, sign, eps, residual_bits=None, po
     normed = bf16_bits(_rms(bf16_to_f32(h).astype(np.float64), weight_bits, eps))
     x_i8, a_scale = rotate_quant_act(normed, sign) if sign is not None else (None, None)
     return x_i8, a_scale, h, normed
+
+
+def lora_add(y, x, ids, a, b, scale):
+    """y + scale[id] (x A[id]^T) B[id]^T in float64 -> (out, bound parts): out
+    [M, N], and for an error bound the magnitudes |B| (|x| |A|) and |B| |v|, both
+    times |scale|, zero for tokens without an adapter."""
+    y, x, a, b = (np.asarray(t, np.float64) for t in (y, x, a, b))
+    out, mag_x, mag_v = y.copy(), np.zeros_like(y), np.zeros_like(y)
+    for t, i in enumerate(ids):
+        if 0 <= i < len(a):
+            v = a[i] @ x[t]
+            s = float(scale[i])
+            out[t] += s * (b[i] @ v)
+            mag_x[t] = abs(s) * (np.abs(b[i]) @ (np.abs(a[i]) @ np.abs(x[t])))
+            mag_v[t] = abs(s) * (np.abs(b[i]) @ np.abs(v))
+    return out, mag_x, mag_v

@@ -45,6 +45,9 @@ SIGNATURES = [
     ("twl_rotate_quant_linear_fused", _INT, [_I64, _I64, _I64]),
     ("twl_norm_rotate_quant_act", _INT,
      [_P, _P, _P, _P, _I64, _F64, _P, _F64, _P, _I64, _I64, _P, _P, _P, _P, _P]),
+    ("twl_lora_add", _INT,
+     [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _INT, _P, _P, _SIZE, _P]),
+    ("twl_lora_workspace_bytes", _SIZE, [_I64, _I64, _I64, _I64]),
     ("twl_last_error", ctypes.c_char_p, []),
     ("twl_abi_version", _INT, []),
 ]

@@ -105,3 +105,51 @@ def norm_rotate_quant_act(x, weight, sign, eps=1e-6, residual=None, post_weight=
         p["sign"], M, K, p["h"], p["normed"], p["x_i8"], p["a_scale"], handle)
     _lib.check(st, "twl_norm_rotate_quant_act")
     return x_i8, a_scale, h, normed
+
+
+def lora_workspace_bytes(M, K, R, n_adapters):
+    """Bytes of workspace lora_add needs for these sizes on the current device."""
+    return int(_lib.load().twl_lora_workspace_bytes(M, K, R, n_adapters))
+
+
+def lora_add(y, x, ids, lora_a, lora_b, scale, out=None, workspace=None, stream=None):
+    """y + scale[id] * (x A[id]^T) B[id]^T for each token's adapter id
+    (twl_lora_add): low-rank adapters of many requests beside a shared projection.
+
+    y [M, N] fp32 or bf16, x [M, K] bf16 (the projection's input before the
+    rotation), ids [M] int32 (outside 0 .. n-1: no adapter), lora_a [n, R, K] and
+    lora_b [n, N, R] bf16, scale [n] fp32.  Returns out (a new tensor unless given;
+    y itself for the update in place).  The workspace (uint8,
+    lora_workspace_bytes) is allocated for each call unless given; in a graph
+    capture it then belongs to that graph."""
+    torch = _torch()
+    lib = _lib.load()
+    M, N = _matrix(y, "y")
+    K = _matrix(x, "x")[1]
+    if not isinstance(lora_a, torch.Tensor) or lora_a.dim() != 3:
+        raise ValueError("lora_a must be a tensor [n, R, K]")
+    n, R = lora_a.shape[:2]
+    bf16 = (torch.bfloat16, torch.int16)
+    kinds = {torch.float32: _lib.OUT_F32, torch.bfloat16: _lib.OUT_BF16}
+    if y.dtype not in kinds:
+        raise TypeError(f"y has dtype {y.dtype}, expected float32 or bfloat16")
+    ctx, handle = _on(stream)
+    p_y = _check(y, "y", (M, N), (y.dtype,))
+    p_x = _check(x, "x", (M, K), bf16)
+    p_ids = _check(ids, "ids", (M,), (torch.int32,))
+    p_a = _check(lora_a, "lora_a", (n, R, K), bf16)
+    p_b = _check(lora_b, "lora_b", (n, N, R), bf16)
+    p_scale = _check(scale, "scale", (n,), (torch.float32,))
+    need = lora_workspace_bytes(M, K, R, n)
+    with ctx:
+        if out is None:
+            out = torch.empty((M, N), dtype=y.dtype, device=y.device)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+    p_out = _check(out, "out", (M, N), (y.dtype,))
+    ws, ws_len = None, 0
+    if workspace is not None:
+        ws, ws_len = _check(workspace, "workspace", (workspace.numel(),), (torch.uint8,)), workspace.numel()
+    st = lib.twl_lora_add(p_y, p_x, p_ids, p_a, p_b, p_scale, M, N, K, R, n, kinds[y.dtype], p_out, ws, ws_len, handle)
+    _lib.check(st, "twl_lora_add")
+    return out

@@ -28,7 +28,7 @@ PEAKS_SRC = "peaks.hip"
 PEAKS_LIB_PATH = os.path.join(PKG_DIR, "libtwl_peaks.so")
 
 SOURCES = ["rotate_quant.hip", "pack.hip", "gemm_i8.hip", "gemv.hip", "reference_bf16.hip",
-           "norm_rotate.hip", "api.cpp", "api_block.cpp"]
+           "norm_rotate.hip", "lora.hip", "api.cpp", "api_block.cpp"]
 
 ARCH = "gfx950"
 COMMON_FLAGS = [

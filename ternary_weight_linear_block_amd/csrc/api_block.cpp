@@ -29,9 +29,75 @@ bool overlap(const Range& a, const Range& b) {
     if (!aligned16(p)) return fail(TWL_EALIGN, "%s is not 16-byte aligned", #p);                \
   } while (0)
 
+twl_status check_lora(int64_t M, int64_t K, int64_t R, int64_t n) {
+  TWL_TRY(check_rows("M", M));
+  TWL_TRY(check_rows("n_adapters", n));
+  if (K <= 0 || K % 128 != 0 || K > TWL_MAX_K)
+    return fail(TWL_ESHAPE, "K=%lld must be a positive multiple of 128 of at most %d", static_cast<long long>(K),
+                TWL_MAX_K);
+  if (R < 8 || R % 8 != 0 || R > TWL_LORA_MAX_R)
+    return fail(TWL_ESHAPE, "R=%lld must be a multiple of 8 from 8 to %d", static_cast<long long>(R), TWL_LORA_MAX_R);
+  return TWL_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t twl_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t n_adapters) {
+  twl::DeviceInfo dev;
+  if (check_lora(M, K, R, n_adapters) != TWL_OK || current_device(&dev) != TWL_OK) return 0;
+  ok();
+  return twl::lora_workspace_bytes(M, static_cast<int>(K), static_cast<int>(R), n_adapters, dev);
+}
+
+twl_status twl_lora_add(const void* y, const uint16_t* x, const int32_t* ids, const uint16_t* lora_a,
+                        const uint16_t* lora_b, const float* scale, int64_t M, int64_t N, int64_t K,
+                        int64_t R, int64_t n_adapters, int kind, void* out, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream) {
+  TWL_TRY(check_lora(M, K, R, n_adapters));
+  TWL_TRY(check_rows("N", N));
+  if (kind != TWL_OUT_F32 && kind != TWL_OUT_BF16) return fail(TWL_EINVAL, "kind %d is not fp32 or bf16", kind);
+  if (M == 0 || N == 0) return ok();
+  TWL_REQUIRE_PTR(y);
+  TWL_REQUIRE_PTR(ids);
+  TWL_REQUIRE_PTR(out);
+  if (n_adapters > 0) {
+    TWL_REQUIRE_PTR(x);
+    TWL_REQUIRE_PTR(lora_a);
+    TWL_REQUIRE_PTR(lora_b);
+    TWL_REQUIRE_PTR(scale);
+  }
+  twl::DeviceInfo dev;
+  TWL_TRY(current_device(&dev));
+  const size_t need = twl::lora_workspace_bytes(M, static_cast<int>(K), static_cast<int>(R), n_adapters, dev);
+  TWL_TRY(check_workspace(need, workspace, workspace_bytes));
+  const size_t rows = static_cast<size_t>(M), n = static_cast<size_t>(n_adapters);
+  const size_t y_bytes = rows * N * (kind == TWL_OUT_F32 ? 4 : 2);
+  const Range outs[] = {{out, y_bytes, "out"}, {need > 0 ? workspace : nullptr, need, "workspace"}};
+  const Range in[] = {{y, y_bytes, "y"}, {x, n > 0 ? rows * K * 2 : 0, "x"}, {ids, rows * 4, "ids"},
+                      {lora_a, n * R * K * 2, "lora_a"}, {lora_b, n * N * R * 2, "lora_b"}, {scale, n * 4, "scale"}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 6; ++j)
+      if (overlap(outs[i], in[j]) && !(i == 0 && j == 0 && out == y))
+        return fail(TWL_EINVAL, "%s overlaps %s", outs[i].name, in[j].name);
+  if (overlap(outs[0], outs[1])) return fail(TWL_EINVAL, "out overlaps workspace");
+  twl::LoraArgs a = {};
+  a.y = y;
+  a.x = x;
+  a.ids = ids;
+  a.a = lora_a;
+  a.b = lora_b;
+  a.scale = scale;
+  a.out = out;
+  a.part = static_cast<float*>(workspace);
+  a.M = M;
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.R = static_cast<int>(R);
+  a.n = static_cast<int>(n_adapters);
+  return launched(twl::launch_lora(a, kind == TWL_OUT_BF16, dev, stream), "lora_add");
+}
 
 twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual,
                                      const uint16_t* post_weight, const uint16_t* gate,

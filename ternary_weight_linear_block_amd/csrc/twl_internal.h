@@ -103,4 +103,23 @@ struct NormArgs {
 };
 hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t stream);
 
+// lora_add (include/twl.h).  The caller sets the operands and sizes; the
+// launcher plans the rest.  `part` holds lora_workspace_bytes.
+struct LoraArgs {
+  const void* y;
+  const uint16_t* x;
+  const int32_t* ids;
+  const uint16_t* a;     // [n, R, K]
+  const uint16_t* b;     // [n, N, R]
+  const float* scale;    // [n]
+  void* out;
+  float* part;           // [slices][M][R]
+  int64_t M;
+  int N, K, R, n;
+  int slices, shrink_tiles, shrink_passes;
+  int expand_chunks, expand_rounds, expand_passes;
+};
+size_t lora_workspace_bytes(int64_t M, int K, int R, int64_t n, const DeviceInfo& dev);
+hipError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo& dev, hipStream_t stream);
+
 }  // namespace twl

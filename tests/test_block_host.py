@@ -76,3 +76,48 @@ def test_norm_accepts_on_the_host(lib):
     # the last byte of x_i8 and the first of a_scale next to each other
     assert _norm(lib, a_scale=P[8] + 4096) not in refused
     assert _norm(lib, M=0, x=None, weight=None, sign=None, h=None, normed=None, x_i8=None, a_scale=None) == 0
+
+
+def _lora(lib, **kw):
+    a = dict(y=P[0], x=P[1], ids=P[2], lora_a=P[3], lora_b=P[4], scale=P[5], M=4, N=64, K=1024, R=16, n_adapters=3, kind=0,
+             out=P[6], workspace=P[7], workspace_bytes=1 << 20, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return lib.twl_lora_add(*a.values())
+
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(K=1000), ESHAPE, b"K="),
+    (dict(K=0), ESHAPE, b"K="),
+    (dict(K=65536 + 128), ESHAPE, b"K="),
+    (dict(R=4), ESHAPE, b"R="),
+    (dict(R=12), ESHAPE, b"R="),
+    (dict(R=136), ESHAPE, b"R="),
+    (dict(R=0), ESHAPE, b"R="),
+    (dict(M=-1), EINVAL, b"M="),
+    (dict(N=-1), EINVAL, b"N="),
+    (dict(n_adapters=-1), EINVAL, b"n_adapters="),
+    (dict(kind=1), EINVAL, b"kind"),
+    (dict(kind=3), EINVAL, b"kind"),
+    (dict(y=None), EINVAL, b"y is NULL"),
+    (dict(x=None), EINVAL, b"x is NULL"),
+    (dict(ids=None), EINVAL, b"ids is NULL"),
+    (dict(lora_a=None), EINVAL, b"lora_a is NULL"),
+    (dict(lora_b=None), EINVAL, b"lora_b is NULL"),
+    (dict(scale=None), EINVAL, b"scale is NULL"),
+    (dict(out=None), EINVAL, b"out is NULL"),
+    (dict(x=P[1] + 2), EALIGN, b"x is not"),
+    (dict(out=P[6] + 4), EALIGN, b"out is not"),
+])
+def test_lora_refuses(lib, kw, status, word):
+    assert _lora(lib, **kw) == status
+    assert word in lib.twl_last_error()
+
+
+def test_lora_empty_calls(lib):
+    none = dict(y=None, x=None, ids=None, lora_a=None, lora_b=None, scale=None, out=None, workspace=None, workspace_bytes=0)
+    assert _lora(lib, M=0, **none) == 0
+    assert _lora(lib, N=0, **none) == 0
+    # without adapters the copy needs y, ids and out only
+    assert _lora(lib, n_adapters=0, x=None, lora_a=None, lora_b=None, scale=None) not in (EINVAL, ESHAPE, EALIGN)
+    assert lib.twl_lora_workspace_bytes(4, 1000, 16, 1) == 0

@@ -1,0 +1,197 @@
+"""lora_add on the GPU against the float64 oracle, element by element.
+
+The bound.  u = 2^-24 is fp32's unit roundoff.  A sum of n fp32 terms in any order
+is off by at most n u times the sum of the magnitudes: v by K u (|x| |A|), with
+the slices' sums and the scale included in K + 64.  Two (three) bf16 terms hold v to
+2^-16 (2^-24) of it, and the second product sums R of each: together
+2^-16 (2^-24) + (3 R + 8) u of |v| |B|.  Adding y rounds once in fp32 (u) and once
+to y's type: 2^-8 for bf16, u for fp32, relative to the result."""
+import numpy as np
+import pytest
+
+import oracle.block_oracle as B
+from tests.gpu_helpers import announce, host
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def twl():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import ternary_weight_linear_block_amd as m
+    m.library()
+    return m
+
+
+def _case(seed, M, N, K, R, n, dtype, ids):
+    rng = np.random.default_rng(seed)
+    t = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32))  # noqa: E731
+    ids = np.asarray(ids(rng, M, n) if callable(ids) else ids, np.int32)
+    return dict(y=t(M, N).to(dtype).cuda(), x=t(M, K).to(torch.bfloat16).cuda(), ids=torch.from_numpy(ids).cuda(),
+                lora_a=(t(n, R, K) / K ** 0.5).to(torch.bfloat16).cuda(), lora_b=t(n, N, R).to(torch.bfloat16).cuda(),
+                scale=torch.from_numpy(rng.uniform(0.5, 2.0, n).astype(np.float32)).cuda())
+
+
+def _np(t):
+    return host(t.float()).astype(np.float64)
+
+
+def _check(out, c, rows=None, y=None):
+    want, mag_x, mag_v = B.lora_add(_np(c["y"] if y is None else y), _np(c["x"]), host(c["ids"]), _np(c["lora_a"]),
+                                    _np(c["lora_b"]), host(c["scale"]))
+    K, R = c["x"].shape[1], c["lora_a"].shape[1]
+    bf16 = c["y"].dtype == torch.bfloat16
+    delta = (K + 64) * U * mag_x + ((2.0 ** -16 if bf16 else 2.0 ** -24) + (3 * R + 8) * U) * mag_v
+    tol = delta + (np.abs(want) + delta) * ((2.0 ** -8 if bf16 else U) + U)
+    got = _np(out)
+    rows = range(len(got)) if rows is None else rows
+    err = np.abs(got - want)[rows]
+    bad = np.argwhere(~(err <= tol[rows]))
+    assert bad.size == 0, f"{len(bad)} off, first {bad[:4].tolist()}, err {err[tuple(bad[0])]:.3g} tol {tol[rows][tuple(bad[0])]:.3g}"
+    none = [t for t, i in enumerate(host(c["ids"])) if not 0 <= i < c["lora_a"].shape[0]]
+    assert torch.equal(out[none], (c["y"] if y is None else y)[none])
+
+
+def mixed(rng, M, n):
+    return rng.integers(-1, n, M)
+
+
+def runs(rng, M, n):
+    return np.repeat(rng.integers(-1, n, M), rng.integers(1, 40, M))[:M]
+
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K,R,n,ids", [
+    (1, 64, 1024, 8, 1, [0]),
+    (1, 5120, 5120, 16, 4, [3]),
+    (1, 130, 128, 16, 2, [1]),
+    (3, 1, 256, 16, 2, [1, 0, 1]),
+    (16, 33, 1024, 24, 3, mixed),
+    (17, 1001, 2048, 40, 5, mixed),
+    (24, 2048, 1024, 16, 32, mixed),
+    (64, 520, 1024, 64, 3, runs),
+    (65, 264, 1024, 72, 4, runs),
+    (200, 1032, 2048, 128, 6, runs),
+    (333, 16400, 1024, 32, 4, runs),
+    (300, 16501, 256, 96, 9, mixed),
+    (130, 32768, 128, 128, 2, runs),
+    (128, 33000, 128, 64, 3, mixed),
+])
+def test_values(twl, M, N, K, R, n, ids, dtype):
+    announce(f"lora M={M} N={N} K={K} R={R} n={n} {dtype}")
+    c = _case(M + N + R, M, N, K, R, n, dtype, ids)
+    _check(twl.lora_add(**c), c)
+
+
+@pytest.mark.parametrize("M,N", [(5, 136), (70, 136), (260, 16384)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_in_place_and_no_adapter(twl, M, N, dtype):
+    """y updated in place; every token without an adapter, also by ids out of range."""
+    c = _case(M, M, N, 512, 16, 3, dtype, mixed)
+    y = c["y"].clone()
+    announce(f"lora in place M={M} N={N} {dtype}")
+    out = twl.lora_add(out=c["y"], **c)
+    assert out is c["y"]
+    _check(out, c, y=y)
+    c = _case(M, M, N, 512, 16, 3, dtype, [(-1, 3, 2 ** 31 - 1, -2 ** 31)[t % 4] for t in range(M)])
+    announce(f"lora no adapter M={M}")
+    assert torch.equal(twl.lora_add(**c), c["y"])
+    empty = dict(c, lora_a=c["lora_a"][:0], lora_b=c["lora_b"][:0], scale=c["scale"][:0])
+    assert torch.equal(twl.lora_add(**empty), c["y"])
+
+
+def test_same_adapter_everywhere_and_twice(twl):
+    """One adapter for all tokens; the same token rows twice give the same rows."""
+    c = _case(1, 96, 16400, 1024, 64, 2, BF, [1] * 96)
+    for k in ("x", "y"):
+        c[k][48:] = c[k][:48]
+    announce("lora one adapter")
+    out = twl.lora_add(**c)
+    _check(out, c)
+    assert torch.equal(out[48:], out[:48])
+    assert torch.equal(out, twl.lora_add(**c))
+
+
+@pytest.mark.parametrize("M,N", [(20, 72), (80, 16392)])
+def test_nan_stays_with_its_users(twl, M, N):
+    """NaN and infinities in one adapter, one token and the unused adapter reach
+    their own tokens' rows only."""
+    ids = [t % 4 for t in range(M)]
+    c = _case(M, M, N, 256, 16, 5, F32, ids)
+    c["lora_a"][2, 3, 7] = float("nan")
+    c["lora_b"][2, :, 1] = float("inf")
+    c["lora_a"][4] = float("nan")
+    c["lora_b"][4] = float("nan")
+    c["x"][5] = float("inf")
+    announce(f"lora nan M={M}")
+    out = twl.lora_add(**c)
+    fine = [t for t in range(M) if ids[t] != 2 and t != 5]
+    with np.errstate(invalid="ignore"):
+        _check(out, c, rows=fine)
+    assert not torch.isfinite(out[2]).any()
+
+
+def test_rows_behind_the_last_stay(twl):
+    c = _case(4, 21, 200, 256, 16, 3, BF, mixed)
+    buf = torch.full((24, 200), 7.0, dtype=BF, device="cuda")
+    ws = torch.full((twl.lora_workspace_bytes(21, 256, 16, 3) + 64,), 0x7F, dtype=torch.uint8, device="cuda")
+    announce("lora guard rows")
+    _check(twl.lora_add(out=buf[:21], workspace=ws, **c), c)
+    assert torch.all(buf[21:] == 7.0).item()
+    assert torch.all(ws[-64:] == 0x7F).item()
+
+
+def test_two_streams_and_graphs(twl):
+    """Calls on two streams at once, and two graphs replayed at once, keep their
+    own workspaces; replays follow changed inputs and ids."""
+    cases = [_case(7 + k, 200, 1024, 2048, 32, 4, F32, runs) for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    announce("lora two streams")
+    outs = [twl.lora_add(stream=s, **c) for s, c in zip(streams, cases)]
+    torch.cuda.synchronize()
+    for o, c in zip(outs, cases):
+        _check(o, c)
+    announce("lora two graphs")
+    graphs = []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = twl.lora_add(**c)
+        graphs.append((g, o))
+    for k in range(3):
+        for i, c in enumerate(cases):
+            new = _case(50 + 2 * k + i, 200, 1024, 2048, 32, 4, F32, mixed if k else runs)
+            for name in c:
+                c[name].copy_(new[name])
+        torch.cuda.synchronize()
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, o), c in zip(graphs, cases):
+            _check(o, c)
+
+
+def test_python_refusals(twl):
+    c = _case(3, 4, 64, 256, 16, 2, F32, [0, 1, 0, 1])
+    bad = [dict(y=c["y"].half()), dict(x=c["x"].float()), dict(x=c["x"][:3]), dict(ids=c["ids"].long()), dict(ids=c["ids"][:3]),
+           dict(lora_a=c["lora_a"][0]), dict(lora_b=c["lora_b"][:1]), dict(lora_b=c["lora_b"].transpose(1, 2)),
+           dict(scale=c["scale"].double()), dict(out=c["y"].bfloat16()), dict(out=c["y"][:2]), dict(out=c["y"].cpu()),
+           dict(lora_a=c["lora_a"][:, :12].contiguous(), lora_b=c["lora_b"][..., :12].contiguous()),
+           dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           dict(workspace=c["y"].view(torch.uint8).view(-1))]
+    for kw in bad:
+        with pytest.raises((ValueError, TypeError, twl.TwlError)):
+            twl.lora_add(**{**c, **kw})
+    with pytest.raises(twl.TwlError):  # K not a multiple of 128
+        twl.lora_add(**{**c, "x": c["x"][:, :120].contiguous(), "lora_a": c["lora_a"][..., :120].contiguous()})
+    assert twl.lora_add(**{**c, "y": c["y"][:0], "x": c["x"][:0], "ids": c["ids"][:0]}).shape == (0, 64)

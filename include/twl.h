@@ -372,6 +372,47 @@ twl_status twl_lora_add(const void* y, const uint16_t* x, const int32_t* ids, co
 /* Bytes of workspace twl_lora_add needs on the current device (0 for invalid sizes). */
 size_t twl_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t n_adapters);
 
+/*
+ * pack_ternary_gated -- pack_ternary of the gate and up projections of a gated
+ * block as one weight of 2 N rows: row 2 i is row i of gate, row 2 i + 1 row i of
+ * up (so that both sums of an output meet in one workgroup).
+ *   code_gate, code_up in : int8 [N, K];  s_gate, s_up in: fp16 bits [N, K/128]
+ *   packed out: twl_packed_bytes(2 N, K) bytes;  q out: int8 [2 N, K/128]
+ *   smax   out: fp32 [2 N];  bad_codes: as pack_ternary, of both
+ */
+twl_status twl_pack_ternary_gated(const int8_t* code_gate, const uint16_t* s_gate,
+                                  const int8_t* code_up, const uint16_t* s_up, int64_t N, int64_t K,
+                                  uint8_t* packed, int8_t* q, float* smax, int32_t* bad_codes,
+                                  hipStream_t stream);
+
+/*
+ * ternary_gated_linear -- the gate and up projections of a gated block, the
+ * activation and the product in one kernel:
+ *   g = acc[t,2i] a_scale[t] smax[2i] / 127,  u = the same of row 2 i + 1  (fp32,
+ *   bit for bit what ternary_linear writes for those rows),
+ *   out[t,i] = g / (1 + exp(-g)) * u
+ * in fp32 with the native exponential and reciprocal, within (|g| + 6) 2^-24
+ * relative (0 where the logistic of g is below 2^-126), rounded once.  Unlike
+ * silu_mul_rotate_quant_act after a bf16 projection, g and u are not rounded and
+ * never written.
+ *   x_i8 [M, K], a_scale [M]: as rotate_quant_act leaves them
+ *   packed, q, smax: as pack_ternary_gated leaves them
+ *   out     : [M, N], fp32 or bf16 by out_kind (TWL_OUT_F32, TWL_OUT_BF16)
+ *   path    : TWL_PATH_AUTO, or TWL_PATH_GEMM / TWL_PATH_GEMV (M <= TWL_GEMV_MAX_M)
+ *             to force the family; all give the same bits
+ *   workspace: twl_gated_workspace_bytes(M, N, K) bytes (covers every path),
+ *             contents on entry do not matter; calls sharing one must not run
+ *             concurrently
+ * N is at most 2^29.  Other errors as ternary_linear_ex.
+ */
+twl_status twl_ternary_gated_linear(const int8_t* x_i8, const float* a_scale, const uint8_t* packed,
+                                    const int8_t* q, const float* smax, int64_t M, int64_t N,
+                                    int64_t K, void* out, int out_kind, int path, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace twl_ternary_gated_linear may need on the current device. */
+size_t twl_gated_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* twl_last_error(void);
 

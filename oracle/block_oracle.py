@@ -3,7 +3,7 @@ definitions of include/twl.h in float64 NumPy, written without the kernels'
 splits and layouts."""
 import numpy as np
 
-from .twl_oracle import bf16_to_f32, round_bf16, rotate_quant_act
+from .twl_oracle import bf16_to_f32, linear_acc, round_bf16, rotate_quant_act
 
 
 def bf16_bits(v: np.ndarray) -> np.ndarray:
@@ -46,3 +46,14 @@ def lora_add(y, x, ids, a, b, scale):
             mag_x[t] = abs(s) * (np.abs(b[i]) @ (np.abs(a[i]) @ np.abs(x[t])))
             mag_v[t] = abs(s) * (np.abs(b[i]) @ np.abs(v))
     return out, mag_x, mag_v
+
+
+def gated_linear(x_i8, a_scale, code_gate, q_gate, smax_gate, code_up, q_up, smax_up):
+    """SiLU(gate) * up of the two projections in float64 -> (out, |gate|, |up|)."""
+    def project(code, q, smax):
+        acc = linear_acc(x_i8, code, q).astype(np.float64)
+        return acc * np.asarray(a_scale, np.float64)[:, None] * np.asarray(smax, np.float64)[None, :] / 127.0
+
+    g, u = project(code_gate, q_gate, smax_gate), project(code_up, q_up, smax_up)
+    with np.errstate(over="ignore"):
+        return g / (1.0 + np.exp(-g)) * u, np.abs(g), np.abs(u)

@@ -8,7 +8,8 @@ Three operations, each one call into the C ABI declared in include/twl.h
   ternary_linear(x_i8, a_scale, packed, q, smax) -> y
 
 The operators of the block around them are in block.py: norm_rotate_quant_act
-(norms, gate, residual and the rotation in one pass) and lora_add (low-rank
+(norms, gate, residual and the rotation in one pass), ternary_gated_linear (gate
+and up projections, SiLU and product in one kernel) and lora_add (low-rank
 adapters of many requests beside a projection).
 
 PyTorch provides device memory and the current stream.  Tensors must be CUDA
@@ -30,7 +31,8 @@ __all__ = [
     "workspace_bytes", "packed_bytes", "plan_info", "TwlError", "PATH_AUTO", "PATH_GEMM", "PATH_GEMV", "PATH_GEMV_DOT4",
     "PATH_GEMV_MFMA", "GEMV_MAX_M",
     "HBLOCK", "GROUP", "MAX_K", "library",
-    "norm_rotate_quant_act", "lora_add", "lora_workspace_bytes",
+    "norm_rotate_quant_act", "lora_add", "lora_workspace_bytes", "pack_ternary_gated",
+    "ternary_gated_linear", "gated_workspace_bytes",
 ]
 
 
@@ -337,4 +339,5 @@ def ternary_linear_acc(x_i8, packed, q, path: int = PATH_AUTO, out=None, workspa
 
 
 # the block operators around the linear layer
-from .block import lora_add, lora_workspace_bytes, norm_rotate_quant_act  # noqa: E402
+from .block import (gated_workspace_bytes, lora_add, lora_workspace_bytes, norm_rotate_quant_act,  # noqa: E402
+                    pack_ternary_gated, ternary_gated_linear)

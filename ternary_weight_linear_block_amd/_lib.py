@@ -48,6 +48,10 @@ SIGNATURES = [
     ("twl_lora_add", _INT,
      [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _INT, _P, _P, _SIZE, _P]),
     ("twl_lora_workspace_bytes", _SIZE, [_I64, _I64, _I64, _I64]),
+    ("twl_pack_ternary_gated", _INT, [_P, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P]),
+    ("twl_ternary_gated_linear", _INT,
+     [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _INT, _INT, _P, _SIZE, _P]),
+    ("twl_gated_workspace_bytes", _SIZE, [_I64, _I64, _I64]),
     ("twl_last_error", ctypes.c_char_p, []),
     ("twl_abi_version", _INT, []),
 ]

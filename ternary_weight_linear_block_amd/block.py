@@ -153,3 +153,72 @@ def lora_add(y, x, ids, lora_a, lora_b, scale, out=None, workspace=None, stream=
     st = lib.twl_lora_add(p_y, p_x, p_ids, p_a, p_b, p_scale, M, N, K, R, n, kinds[y.dtype], p_out, ws, ws_len, handle)
     _lib.check(st, "twl_lora_add")
     return out
+
+
+def pack_ternary_gated(code_gate, s_gate, code_up, s_up, bad_codes=None, stream=None):
+    """Gate and up codes [N, K] int8 and scales [N, K/128] fp16 -> (packed, q
+    [2 N, K/128], smax [2 N]) of ternary_gated_linear (twl_pack_ternary_gated)."""
+    torch = _torch()
+    lib = _lib.load()
+    N, K = _matrix(code_gate, "code_gate")
+    fp16 = (torch.float16, torch.int16)
+    ctx, handle = _on(stream)
+    G = K // _lib.GROUP
+    ptrs = [_check(code_gate, "code_gate", (N, K), (torch.int8,)), _check(s_gate, "s_gate", (N, G), fp16),
+            _check(code_up, "code_up", (N, K), (torch.int8,)), _check(s_up, "s_up", (N, G), fp16)]
+    bad = None if bad_codes is None else _check(bad_codes, "bad_codes", bad_codes.shape, (torch.int32,))
+    if bad_codes is not None and bad_codes.numel() < 1:
+        raise ValueError("bad_codes is empty")
+    with ctx:
+        packed = torch.empty((int(lib.twl_packed_bytes(2 * N, K)),), dtype=torch.uint8, device=code_gate.device)
+        q = torch.empty((2 * N, G), dtype=torch.int8, device=code_gate.device)
+        smax = torch.empty((2 * N,), dtype=torch.float32, device=code_gate.device)
+    st = lib.twl_pack_ternary_gated(*ptrs, N, K, packed.data_ptr(), q.data_ptr(), smax.data_ptr(), bad, handle)
+    _lib.check(st, "twl_pack_ternary_gated")
+    return packed, q, smax
+
+
+def gated_workspace_bytes(M, N, K):
+    """Bytes of workspace ternary_gated_linear may need for these sizes on the current device."""
+    return int(_lib.load().twl_gated_workspace_bytes(M, N, K))
+
+
+def ternary_gated_linear(x_i8, a_scale, packed, q, smax, out_dtype=None, path=_lib.PATH_AUTO, out=None,
+                         workspace=None, stream=None):
+    """SiLU(gate) * up of the two ternary projections that pack_ternary_gated packed,
+    for the int8 activations of rotate_quant_act or norm_rotate_quant_act
+    (twl_ternary_gated_linear).
+
+    Returns out [M, N], bf16 unless out_dtype (or the given out) is float32.  The
+    workspace (uint8, gated_workspace_bytes) is allocated for each call that needs
+    one unless given; in a graph capture it then belongs to that graph."""
+    torch = _torch()
+    lib = _lib.load()
+    M, K = _matrix(x_i8, "x_i8")
+    N2, G = _matrix(q, "q")
+    if N2 % 2:
+        raise ValueError(f"q has {N2} rows, expected 2 N of pack_ternary_gated")
+    N = N2 // 2
+    kinds = {torch.float32: _lib.OUT_F32, torch.bfloat16: _lib.OUT_BF16}
+    dtype = out_dtype if out_dtype is not None else out.dtype if out is not None else torch.bfloat16
+    if dtype not in kinds:
+        raise TypeError(f"out_dtype is {dtype}, expected float32 or bfloat16")
+    ctx, handle = _on(stream)
+    p_x = _check(x_i8, "x_i8", (M, K), (torch.int8,))
+    p_a = _check(a_scale, "a_scale", (M,), (torch.float32,))
+    p_w = _check(packed, "packed", (int(lib.twl_packed_bytes(N2, K)),), (torch.uint8,))
+    p_q = _check(q, "q", (N2, K // _lib.GROUP), (torch.int8,))
+    p_s = _check(smax, "smax", (N2,), (torch.float32,))
+    need = gated_workspace_bytes(M, N, K)
+    with ctx:
+        if out is None:
+            out = torch.empty((M, N), dtype=dtype, device=x_i8.device)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x_i8.device)
+    p_out = _check(out, "out", (M, N), (dtype,))
+    ws, ws_len = None, 0
+    if workspace is not None:
+        ws, ws_len = _check(workspace, "workspace", (workspace.numel(),), (torch.uint8,)), workspace.numel()
+    st = lib.twl_ternary_gated_linear(p_x, p_a, p_w, p_q, p_s, M, N, K, p_out, kinds[dtype], path, ws, ws_len, handle)
+    _lib.check(st, "twl_ternary_gated_linear")
+    return out

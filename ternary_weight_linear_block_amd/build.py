@@ -27,7 +27,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libtwl.so")
 PEAKS_SRC = "peaks.hip"
 PEAKS_LIB_PATH = os.path.join(PKG_DIR, "libtwl_peaks.so")
 
-SOURCES = ["rotate_quant.hip", "pack.hip", "gemm_i8.hip", "gemv.hip", "reference_bf16.hip",
+SOURCES = ["rotate_quant.hip", "pack.hip", "gemm_i8.hip", "gemv.hip", "gemv_gated.hip", "reference_bf16.hip",
            "norm_rotate.hip", "lora.hip", "api.cpp", "api_block.cpp"]
 
 ARCH = "gfx950"

@@ -40,9 +40,89 @@ twl_status check_lora(int64_t M, int64_t K, int64_t R, int64_t n) {
   return TWL_OK;
 }
 
+// Sizes of a gated pair of N x K projections (2 N packed rows).
+twl_status check_gated(int64_t N, int64_t K) {
+  TWL_TRY(check_rows("N", N));
+  if (N > (int64_t{1} << 29)) return fail(TWL_ESHAPE, "N=%lld is too large", static_cast<long long>(N));
+  return check_k(K);
+}
+
+// Whether this path runs a decode kernel at M tokens, and its workspace.
+bool gated_decodes(int64_t M, int path) {
+  return path == TWL_PATH_GEMV || (path == TWL_PATH_AUTO && M <= TWL_GEMV_MAX_M);
+}
+
+size_t gated_need(int64_t M, int64_t N, int64_t K, int path, const twl::DeviceInfo& dev) {
+  return gated_decodes(M, path) ? twl::gemv_gated_workspace_bytes(M, 2 * N, K, dev)
+                                : twl::gemm_workspace_bytes(M, 2 * N, K, dev);
+}
+
 }  // namespace
 
 extern "C" {
+
+twl_status twl_pack_ternary_gated(const int8_t* code_gate, const uint16_t* s_gate,
+                                  const int8_t* code_up, const uint16_t* s_up, int64_t N, int64_t K,
+                                  uint8_t* packed, int8_t* q, float* smax, int32_t* bad_codes,
+                                  hipStream_t stream) {
+  TWL_TRY(check_gated(N, K));
+  if (N == 0) return ok();
+  TWL_REQUIRE_PTR(code_gate);
+  TWL_REQUIRE_PTR(s_gate);
+  TWL_REQUIRE_PTR(code_up);
+  TWL_REQUIRE_PTR(s_up);
+  TWL_REQUIRE_PTR(packed);
+  TWL_REQUIRE_PTR(q);
+  TWL_REQUIRE_PTR(smax);
+  if (bad_codes != nullptr && (reinterpret_cast<uintptr_t>(bad_codes) & 3u))
+    return fail(TWL_EALIGN, "bad_codes is not 4-byte aligned");
+  twl::DeviceInfo dev;
+  TWL_TRY(current_device(&dev));
+  return launched(twl::launch_pack_gated(code_gate, s_gate, code_up, s_up, N, K, packed, q, smax, bad_codes, stream),
+                  "pack_ternary_gated");
+}
+
+size_t twl_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  twl::DeviceInfo dev;
+  if (M <= 0 || N <= 0 || check_rows("M", M) != TWL_OK || check_gated(N, K) != TWL_OK ||
+      current_device(&dev) != TWL_OK)
+    return 0;
+  size_t need = gated_need(M, N, K, TWL_PATH_GEMM, dev);
+  if (M <= TWL_GEMV_MAX_M) need = std::max(need, gated_need(M, N, K, TWL_PATH_GEMV, dev));
+  return need;
+}
+
+twl_status twl_ternary_gated_linear(const int8_t* x_i8, const float* a_scale, const uint8_t* packed,
+                                    const int8_t* q, const float* smax, int64_t M, int64_t N,
+                                    int64_t K, void* out, int out_kind, int path, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream) {
+  TWL_TRY(check_rows("M", M));
+  TWL_TRY(check_gated(N, K));
+  if (path != TWL_PATH_AUTO && path != TWL_PATH_GEMM && path != TWL_PATH_GEMV)
+    return fail(TWL_EINVAL, "path %d is not AUTO, GEMM or GEMV", path);
+  if (out_kind != TWL_OUT_F32 && out_kind != TWL_OUT_BF16)
+    return fail(TWL_EINVAL, "output kind %d is not fp32 or bf16", out_kind);
+  if (path == TWL_PATH_GEMV && M > TWL_GEMV_MAX_M)
+    return fail(TWL_ESHAPE, "the decode path takes M <= %d (got %lld)", TWL_GEMV_MAX_M, static_cast<long long>(M));
+  if (M == 0 || N == 0) return ok();
+  TWL_REQUIRE_PTR(x_i8);
+  TWL_REQUIRE_PTR(a_scale);
+  TWL_REQUIRE_PTR(packed);
+  TWL_REQUIRE_PTR(q);
+  TWL_REQUIRE_PTR(smax);
+  TWL_REQUIRE_PTR(out);
+  twl::DeviceInfo dev;
+  TWL_TRY(current_device(&dev));
+  const size_t need = gated_need(M, N, K, path, dev);
+  TWL_TRY(check_workspace(need, workspace, workspace_bytes));
+  const twl::OutKind kind = out_kind == TWL_OUT_BF16 ? twl::kOutGatedBf16 : twl::kOutGatedF32;
+  if (gated_decodes(M, path))
+    return launched(twl::launch_gemv_gated(x_i8, a_scale, packed, q, smax, M, 2 * N, K, out, kind, workspace, dev, stream),
+                    "ternary_gated_linear (GEMV)");
+  return launched(twl::launch_gemm(x_i8, a_scale, packed, q, smax, M, 2 * N, K, out, kind, workspace, workspace_bytes, dev,
+                                   stream),
+                  "ternary_gated_linear (GEMM)");
+}
 
 size_t twl_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t n_adapters) {
   twl::DeviceInfo dev;

@@ -55,6 +55,10 @@
 //     same weights) land on the same XCD and its L2.
 //   * The stage loop is unrolled by the pipeline depth, so buffer offsets are
 //     constants and the packed words alternate between two register sets.
+//   * Gated outputs (ternary_gated_linear): gate and up rows alternate in the
+//     packed weight, so a gate and its up are adjacent columns of one tile; they
+//     meet in the output transpose, where a lane reads 8 columns and stores 4
+//     results.  Neither projection leaves the chip.
 //   * Output: each kept 16x32 half fragment is transposed through a per-wave
 //     LDS scratch (two buffers, alternated) so that every lane writes 16
 //     contiguous bytes (fp32 / int32 y: 4 columns; bf16 y: 8 columns): the
@@ -241,6 +245,34 @@ __device__ __forceinline__ void lds_wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Four results of eight adjacent gated columns (gate, up, gate, up, ..., as fp32 bit
+// patterns) at row `row` of out [M, I], columns c .. c + 3; those past `end` are
+// not stored.
+template <int OUT>
+__device__ __forceinline__ void store_gated4(void* out, size_t row, int I, int c, int end, const v4i& a, const v4i& b) {
+  const float h[4] = {silu_mul(__int_as_float(a.x), __int_as_float(a.y)), silu_mul(__int_as_float(a.z), __int_as_float(a.w)),
+                      silu_mul(__int_as_float(b.x), __int_as_float(b.y)), silu_mul(__int_as_float(b.z), __int_as_float(b.w))};
+  const size_t o = row * I + c;
+  if ((I & 3) == 0) {  // c and end are multiples of 4: all four are in range or none
+    if (c >= end) return;
+    if (OUT == kOutGatedBf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + o) =
+          make_uint2(f32_to_bf16_rne(h[0]) | (static_cast<uint32_t>(f32_to_bf16_rne(h[1])) << 16),
+                     f32_to_bf16_rne(h[2]) | (static_cast<uint32_t>(f32_to_bf16_rne(h[3])) << 16));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = make_float4(h[0], h[1], h[2], h[3]);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c + e < end) {
+      if (OUT == kOutGatedBf16)
+        static_cast<uint16_t*>(out)[o + e] = f32_to_bf16_rne(h[e]);
+      else
+        static_cast<float*>(out)[o + e] = h[e];
+    }
+}
+
 // Stores one 32x32 fragment of one wave (MFMA layout: lane l32 = column,
 // register r = row 8 (r / 4) + 4 (lane / 32) + r % 4) with its epilogue.
 // row0/col0: the fragment's first output row and column; rs/cs: the scales of
@@ -253,7 +285,7 @@ __device__ __forceinline__ void store_frag(const v16i& acc, void* out, const flo
                                            int M, int N, int row0, int col0, int lane, int32_t* tr) {
   const int l32 = lane & 31, half = lane >> 5;
   const float cscale = OUT == kOutAcc ? 0.0f : cs[l32] * (1.0f / 127.0f);
-  if ((N & 3) != 0) {
+  if (!is_gated(OUT) && (N & 3) != 0) {
     const int col = col0 + l32;
     if (col >= N) return;
 #pragma unroll
@@ -272,6 +304,17 @@ __device__ __forceinline__ void store_frag(const v16i& acc, void* out, const flo
         OUT == kOutAcc ? acc[r] : __float_as_int(static_cast<float>(acc[r]) * rs[rr] * cscale);
   }
   lds_wave_sync();
+  if constexpr (is_gated(OUT)) {
+    const int c8 = 8 * (lane & 3);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int rr = 16 * k + (lane >> 2);
+      const v4i a = *reinterpret_cast<const v4i*>(tr + rr * kTrStride + c8);
+      const v4i b = *reinterpret_cast<const v4i*>(tr + rr * kTrStride + c8 + 4);
+      if (row0 + rr < M) store_gated4<OUT>(out, static_cast<size_t>(row0 + rr), N / 2, (col0 + c8) / 2, N / 2, a, b);
+    }
+    return;
+  }
   if (OUT == kOutBf16 && (N & 7) == 0) {
     // 8 columns per lane: one 16-byte store covers 16 rows of the fragment
     const int c8 = 8 * (lane & 3);
@@ -428,7 +471,7 @@ __device__ __forceinline__ void finish_tile(v16i (&acc)[RM][(FN + WN - 1) / WN],
   static_assert(WK == 2, "the output path covers one register half per wave (wave pairs)");
   const int M = p.M, N = p.N, m0 = w.m0, n0 = w.n0;
   const int n_end = min(N, n0 + p.tile_sn);  // columns this tile stores
-  if ((N & 3) != 0) {
+  if (!is_gated(OUT) && (N & 3) != 0) {
     // rare shapes: element stores straight from the registers
 #pragma unroll
     for (int q = 0; q < NF; ++q) {
@@ -450,7 +493,8 @@ __device__ __forceinline__ void finish_tile(v16i (&acc)[RM][(FN + WN - 1) / WN],
   constexpr int kHalfWords = 16 * kTrStride;  // one transpose buffer
   static_assert(T::LDS_BYTES >= T::NW * 2 * kHalfWords * 4, "LDS too small for the output transposes");
   int32_t* tr0 = reinterpret_cast<int32_t*>(smem) + wave * 2 * kHalfWords;
-  const bool bf16x8 = OUT == kOutBf16 && (N & 7) == 0;
+  // 8 columns of 16 rows a lane instead of 4 columns of 8, twice
+  const bool bf16x8 = is_gated(OUT) || (OUT == kOutBf16 && (N & 7) == 0);
   v4i rd[2][2];
   // transpose kept half-fragment q through buffer b into rd[b]
   const auto stage = [&](int q, int b) {
@@ -481,6 +525,11 @@ __device__ __forceinline__ void finish_tile(v16i (&acc)[RM][(FN + WN - 1) / WN],
     const int f = wn * RN + q % RN;
     if (FN % WN != 0 && f >= FN) return;  // padding fragment (wave-uniform)
     const int grow0 = m0 + wm * 32 * RM + 32 * (q / RN) + row_off;
+    if constexpr (is_gated(OUT)) {
+      const int grow = grow0 + (lane >> 2), gcol = n0 + 32 * f + 8 * (lane & 3);
+      if (grow < M) store_gated4<OUT>(p.out, static_cast<size_t>(grow), N / 2, gcol / 2, n_end / 2, rd[b][0], rd[b][1]);
+      return;
+    }
     if (bf16x8) {
       const int grow = grow0 + (lane >> 2), gcol = n0 + 32 * f + 8 * (lane & 3);
       if (grow < M && gcol < n_end)
@@ -923,6 +972,8 @@ hipError_t launch_cfg(const GemmArgs& a, OutKind out_kind, hipStream_t stream) {
   switch (out_kind) {
     case kOutAcc: return launch_cfg_out<RM, FN, WK, WN, kOutAcc>(a, stream);
     case kOutBf16: return launch_cfg_out<RM, FN, WK, WN, kOutBf16>(a, stream);
+    case kOutGatedF32: return launch_cfg_out<RM, FN, WK, WN, kOutGatedF32>(a, stream);
+    case kOutGatedBf16: return launch_cfg_out<RM, FN, WK, WN, kOutGatedBf16>(a, stream);
     default: return launch_cfg_out<RM, FN, WK, WN, kOutF32>(a, stream);
   }
 }

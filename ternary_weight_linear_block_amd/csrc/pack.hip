@@ -38,8 +38,13 @@ __device__ __forceinline__ float fp16_bits_to_float(uint16_t bits) {
   return static_cast<float>(__builtin_bit_cast(_Float16, bits));
 }
 
+// GATED: N rows taken from two layers in turn, row n from row n / 2 of (code, s) for
+// even n and of (code_up, s_up) for odd.
+template <bool GATED>
 __global__ __launch_bounds__(256) void pack_kernel(const int8_t* __restrict__ code,
-                                                   const uint16_t* __restrict__ s, int N, int K,
+                                                   const uint16_t* __restrict__ s,
+                                                   const int8_t* __restrict__ code_up,
+                                                   const uint16_t* __restrict__ s_up, int N, int K,
                                                    uint8_t* __restrict__ packed,
                                                    int8_t* __restrict__ q,
                                                    float* __restrict__ smax,
@@ -56,7 +61,9 @@ __global__ __launch_bounds__(256) void pack_kernel(const int8_t* __restrict__ co
     return;
   }
 
-  const uint16_t* sr = s + static_cast<size_t>(n) * G;
+  const int src = GATED ? n >> 1 : n;
+  const bool up = GATED && (n & 1) != 0;
+  const uint16_t* sr = (up ? s_up : s) + static_cast<size_t>(src) * G;
   // smax[n] = max_g |s[n,g]|
   float m = 0.0f;
   for (int g = tid; g < G; g += 256) m = fmaxf(m, fabsf(fp16_bits_to_float(sr[g])));
@@ -79,7 +86,7 @@ __global__ __launch_bounds__(256) void pack_kernel(const int8_t* __restrict__ co
 
   // 2-bit packing, one 16-code word per thread iteration; word w of the row is
   // word w % 8 of its row slot in tile (n / 64, w / 8)
-  const int8_t* cr = code + static_cast<size_t>(n) * K;
+  const int8_t* cr = (up ? code_up : code) + static_cast<size_t>(src) * K;
   int nbad = 0;
   for (int w = tid; w < (K >> 4); w += 256) {
     const uint4 c = *reinterpret_cast<const uint4*>(cr + 16 * w);
@@ -124,8 +131,19 @@ hipError_t launch_pack(const int8_t* code, const uint16_t* s, int64_t N, int64_t
                        hipStream_t stream) {
   if (N == 0) return hipSuccess;
   const int64_t rows = (N + 63) / 64 * 64;
-  hipLaunchKernelGGL(pack_kernel, dim3(static_cast<unsigned>(rows)), dim3(256), 0, stream, code, s,
-                     static_cast<int>(N), static_cast<int>(K), packed, q, smax, bad_codes);
+  hipLaunchKernelGGL(pack_kernel<false>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, stream, code, s,
+                     nullptr, nullptr, static_cast<int>(N), static_cast<int>(K), packed, q, smax, bad_codes);
+  return hipGetLastError();
+}
+
+hipError_t launch_pack_gated(const int8_t* code_gate, const uint16_t* s_gate, const int8_t* code_up,
+                             const uint16_t* s_up, int64_t N, int64_t K, uint8_t* packed, int8_t* q,
+                             float* smax, int32_t* bad_codes, hipStream_t stream) {
+  if (N == 0) return hipSuccess;
+  const int64_t rows = (2 * N + 63) / 64 * 64;
+  hipLaunchKernelGGL(pack_kernel<true>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, stream, code_gate,
+                     s_gate, code_up, s_up, static_cast<int>(2 * N), static_cast<int>(K), packed, q, smax,
+                     bad_codes);
   return hipGetLastError();
 }
 

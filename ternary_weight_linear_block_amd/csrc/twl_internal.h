@@ -30,15 +30,33 @@ hipError_t launch_silu_mul_rotate_quant(const uint16_t* gate_up, const int8_t* s
 hipError_t launch_pack(const int8_t* code, const uint16_t* s, int64_t N, int64_t K,
                        uint8_t* packed, int8_t* q, float* smax, int32_t* bad_codes,
                        hipStream_t stream);
+// The same of 2 N rows, gate and up in turn.
+hipError_t launch_pack_gated(const int8_t* code_gate, const uint16_t* s_gate, const int8_t* code_up,
+                             const uint16_t* s_up, int64_t N, int64_t K, uint8_t* packed, int8_t* q,
+                             float* smax, int32_t* bad_codes, hipStream_t stream);
 
 // What the linear layer writes: fp32 y, the raw int32 accumulators, or y
 // rounded to bf16 (round to nearest even).
-enum OutKind { kOutF32 = 0, kOutAcc = 1, kOutBf16 = 2 };
+// The gated kinds (ternary_gated_linear): rows of the weight are gate and up in
+// turn, N = 2 I of them, and out [M, I] is SiLU(gate) * up of adjacent columns.
+enum OutKind { kOutF32 = 0, kOutAcc = 1, kOutBf16 = 2, kOutGatedF32 = 3, kOutGatedBf16 = 4 };
+constexpr bool is_gated(int kind) { return kind >= kOutGatedF32; }
 
 // fp32 -> bf16 bits, round to nearest even (finite inputs).
 __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   const uint32_t u = __float_as_uint(f);
   return static_cast<uint16_t>((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+
+// SiLU(g) u = g u / (1 + e^-g), by the native exponential and reciprocal (1 ulp
+// each).  The rounding of g log2(e) enters e^-g as |g| 2^-24, so the result is
+// within (|g| + 6) 2^-24 relative: below half a bf16 step by a factor of 2^10 at
+// |g| = 50.  Where 1 + e^-g passes 2^126 (g below -87) the reciprocal is below the
+// smallest normal number and comes out as 0.  Every kernel of ternary_gated_linear uses this
+// form, so all of them give the same bits.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const float e = __builtin_amdgcn_exp2f(g * -0x1.715476p+0f);
+  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
 // Stores one epilogue value v (y before rounding) or the accumulator s at
@@ -71,6 +89,23 @@ hipError_t launch_gemv(const int8_t* x_i8, const float* a_scale, const uint8_t* 
 size_t gemv_workspace_bytes(int64_t M, int64_t N, int64_t K, GemvKind kind, const DeviceInfo& dev);
 // The decode plan for this shape, as twl_plan_info reports it (info[0..7]).
 void gemv_plan_info(int64_t M, int64_t N, int64_t K, GemvKind kind, const DeviceInfo& dev, int64_t* info);
+
+// The decode kernels for narrow layers (the dot4 or K-split MFMA kernel by M) up to
+// their int32 partial sums: `part` gets [slices][M][N], slices being returned by
+// gemv_part_slices, and holds that many.
+int gemv_part_slices(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
+hipError_t launch_gemv_part(const int8_t* x_i8, const uint8_t* packed, const int8_t* q, int64_t M,
+                            int64_t N, int64_t K, int32_t* part, const DeviceInfo& dev,
+                            hipStream_t stream);
+
+// ternary_gated_linear for decode batches (M <= 24) of a packed weight of N = 2 I
+// interleaved rows: the row-balanced kernel with whole pairs of rows to a
+// workgroup, or, for narrower layers, launch_gemv_part and a finishing kernel.
+size_t gemv_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
+hipError_t launch_gemv_gated(const int8_t* x_i8, const float* a_scale, const uint8_t* packed,
+                             const int8_t* q, const float* smax, int64_t M, int64_t N, int64_t K,
+                             void* out, OutKind out_kind, void* part, const DeviceInfo& dev,
+                             hipStream_t stream);
 
 // Fused decode: rotate_quant_act (silu: of bf16(SiLU(gate) * up), x being
 // [gate | up] [M, 2K]) and the row-balanced decode kernel in one launch, which

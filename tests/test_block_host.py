@@ -121,3 +121,48 @@ def test_lora_empty_calls(lib):
     # without adapters the copy needs y, ids and out only
     assert _lora(lib, n_adapters=0, x=None, lora_a=None, lora_b=None, scale=None) not in (EINVAL, ESHAPE, EALIGN)
     assert lib.twl_lora_workspace_bytes(4, 1000, 16, 1) == 0
+
+
+def _gated(lib, **kw):
+    a = dict(x_i8=P[0], a_scale=P[1], packed=P[2], q=P[3], smax=P[4], M=4, N=64, K=1024, out=P[5], out_kind=2, path=0,
+             workspace=P[6], workspace_bytes=1 << 20, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return lib.twl_ternary_gated_linear(*a.values())
+
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(K=1000), ESHAPE, b"K="),
+    (dict(M=-1), EINVAL, b"M="),
+    (dict(N=-1), EINVAL, b"N="),
+    (dict(N=(1 << 29) + 1), ESHAPE, b"N="),
+    (dict(out_kind=1), EINVAL, b"output kind"),
+    (dict(out_kind=3), EINVAL, b"output kind"),
+    (dict(path=3), EINVAL, b"path"),
+    (dict(path=-1), EINVAL, b"path"),
+    (dict(path=2, M=25), ESHAPE, b"M <="),
+    (dict(x_i8=None), EINVAL, b"x_i8 is NULL"),
+    (dict(a_scale=None), EINVAL, b"a_scale is NULL"),
+    (dict(packed=None), EINVAL, b"packed is NULL"),
+    (dict(q=None), EINVAL, b"q is NULL"),
+    (dict(smax=None), EINVAL, b"smax is NULL"),
+    (dict(out=None), EINVAL, b"out is NULL"),
+    (dict(out=P[5] + 8), EALIGN, b"out is not"),
+])
+def test_gated_refuses(lib, kw, status, word):
+    assert _gated(lib, **kw) == status
+    assert word in lib.twl_last_error()
+
+
+def test_gated_empty_calls_and_pack(lib):
+    none = dict(x_i8=None, a_scale=None, packed=None, q=None, smax=None, out=None, workspace=None, workspace_bytes=0)
+    assert _gated(lib, M=0, **none) == 0
+    assert _gated(lib, N=0, **none) == 0
+    pack = lib.twl_pack_ternary_gated
+    assert pack(None, None, None, None, 0, 1024, None, None, None, None, None) == 0
+    assert pack(P[0], P[1], P[2], P[3], 8, 1000, P[4], P[5], P[6], None, None) == ESHAPE
+    assert pack(P[0], P[1], None, P[3], 8, 1024, P[4], P[5], P[6], None, None) == EINVAL
+    assert b"code_up is NULL" in lib.twl_last_error()
+    assert pack(P[0], P[1], P[2], P[3] + 2, 8, 1024, P[4], P[5], P[6], None, None) == EALIGN
+    assert pack(P[0], P[1], P[2], P[3], 8, 1024, P[4], P[5], P[6], P[7] + 2, None) == EALIGN
+    assert lib.twl_gated_workspace_bytes(4, 64, 1000) == 0

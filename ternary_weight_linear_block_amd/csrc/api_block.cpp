@@ -244,7 +244,7 @@ twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual
   a.M = M;
   a.gate_stride = gate_stride;
   a.K = static_cast<int>(K);
-  return launched(twl::launch_norm_rotate(a, stream), "norm_rotate_quant_act");
+  return launched(twl::launch_norm_rotate(a, dev, stream), "norm_rotate_quant_act");
 }
 
 }  // extern "C"

@@ -10,16 +10,17 @@
 //   x_i8, a_scale = rotate_quant_act(n)              rotate_block.h, unchanged
 // n is rounded to bf16 because that is what an unfused pipeline stores, what
 // adapters beside the projection read, and what rotate_quant_act takes: the
-// int8 result equals rotate_quant_act(n) bit for bit.  The sums and products are
-// fp64 because a value next to a bf16 rounding border would otherwise round
-// either way with the order of the sum; an element costs about 17 fp64
-// operations, which the memory time covers.
+// int8 result equals rotate_quant_act(n) bit for bit.  The sums are fp64 and every
+// product exact or fp64, because a value next to a bf16 rounding border would
+// otherwise round either way with the order of the sum (fp64 runs at the rate of
+// fp32 here: 4 cycles a wave, conversions too).
 //
-// One workgroup per token, wave w owns the 1024-blocks w, w + nw, ... in the
-// rotation's first layout (lane = 16 consecutive elements), so a row is read
-// once and stays in registers as packed bf16 through both norms and the
-// rotation; the statistics meet in LDS (waves in order, so the sums do not
-// depend on timing).
+// Wave w of a workgroup owns the 1024-blocks w, w + nw, ... of a row, so a row is
+// read once and stays in registers as packed bf16 through both norms and the
+// rotation (which takes it through LDS into its own first layout); the
+// statistics meet in LDS (waves in order, so the sums do not depend on timing).
+// Workgroups stay and take every gridDim.x-th token; with one block a wave the
+// next token's rows are loaded while this one is computed.
 #include "rotate_block.h"
 
 #include <algorithm>
@@ -35,47 +36,106 @@ constexpr int kMaxNormWaves = 16;
 __device__ __forceinline__ double lo_f64(uint32_t w) { return static_cast<double>(__uint_as_float(w << 16)); }
 __device__ __forceinline__ double hi_f64(uint32_t w) { return static_cast<double>(__uint_as_float(w & 0xFFFF0000u)); }
 
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+// fp64 -> fp32 -> bf16, both to nearest even (v_cvt_pk_bf16_f32)
 __device__ __forceinline__ uint32_t pack_bf16(double lo, double hi) {
-  return f32_to_bf16_rne(static_cast<float>(lo)) |
-         (static_cast<uint32_t>(f32_to_bf16_rne(static_cast<float>(hi))) << 16);
+  const v2f f = {static_cast<float>(lo), static_cast<float>(hi)};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, v2bf));
 }
 
-// 16 consecutive bf16 of one lane
+// One lane's 16 bf16 of a 1024-block: elements 8 lane .. + 7 and 512 + 8 lane .. + 7,
+// so that a load or store of the wave covers 1024 consecutive bytes.
 struct Row16 {
   uint32_t w[8];
 };
 
-__device__ __forceinline__ Row16 load16(const uint16_t* p) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint4 b = *reinterpret_cast<const uint4*>(p + 8);
+__device__ __forceinline__ Row16 load16(const uint16_t* block, int lane) {
+  const uint4 a = *reinterpret_cast<const uint4*>(block + 8 * lane);
+  const uint4 b = *reinterpret_cast<const uint4*>(block + 512 + 8 * lane);
   return Row16{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
 
-__device__ __forceinline__ void store16(uint16_t* p, const Row16& r) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-  *reinterpret_cast<uint4*>(p + 8) = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+__device__ __forceinline__ void store16(uint16_t* block, int lane, const Row16& r) {
+  *reinterpret_cast<uint4*>(block + 8 * lane) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+  *reinterpret_cast<uint4*>(block + 512 + 8 * lane) = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
 }
 
-// Sum of squares of a lane's elements.  The empty asm afterwards makes the packed
-// words opaque: without it the compiler keeps their fp64 copies (32 registers a
-// block) from here to their next use and spills.
+// The same 16 values a lane as the rotation wants them, elements 16 lane .. + 15,
+// through the wave's transpose buffer (idle between two rotations).
+__device__ __forceinline__ Row16 consecutive(const Row16& r, int lane, float* wb) {
+  uint4* buf = reinterpret_cast<uint4*>(wb);
+  rot::wave_lds_sync();
+  // 16-byte units, one spare after every eight: the reads hit different banks
+  const auto at = [](int unit) { return unit + (unit >> 3); };
+  buf[at(lane)] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+  buf[at(64 + lane)] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+  rot::wave_lds_sync();
+  const uint4 a = buf[at(2 * lane)], b = buf[at(2 * lane + 1)];
+  return Row16{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+
+// Makes the packed words opaque to the compiler, which otherwise keeps fp64 copies
+// of them (32 registers a block) from one use to the next, or over the whole token
+// loop, and spills.
+__device__ __forceinline__ void opaque(Row16& r) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(r.w[e]));
+}
+
+// Sum of squares of a lane's elements.
 __device__ __forceinline__ double sum_squares(Row16& r) {
   double s = 0.0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const double a = lo_f64(r.w[e]), b = hi_f64(r.w[e]);
-    s += a * a;
-    s += b * b;
+    s = __builtin_fma(a, a, s);
+    s = __builtin_fma(b, b, s);
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(r.w[e]));
+  opaque(r);
   return s;
 }
 
-// Sum over the workgroup, waves added in order; `slots` holds one double a wave.
-__device__ __forceinline__ double block_sum(double s, double* slots, int wave, int lane, int nw) {
+// A row whose mean square is above kLargeMean is multiplied by 2^-64 (exact but
+// for elements 2^-100 below the mean) before its products with the tables, which
+// would otherwise leave fp32's range, and its norm by 2^64.
+constexpr double kLargeMean = 0x1p180, kGrow = 0x1p64;
+
+__device__ __forceinline__ void shrink(Row16& r) {
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m);
+  for (int e = 0; e < 8; ++e) r.w[e] = pack_bf16(lo_f64(r.w[e]) * 0x1p-64, hi_f64(r.w[e]) * 0x1p-64);
+}
+
+// row_ror:n of a wave's four rows of 16 lanes
+template <int N>
+__device__ __forceinline__ uint32_t row_ror(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + N, 0xF, 0xF, true));
+}
+
+template <int N>
+__device__ __forceinline__ double row_ror(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = row_ror<N>(static_cast<uint32_t>(b)), hi = row_ror<N>(static_cast<uint32_t>(b >> 32));
+  return __builtin_bit_cast(double, (hi << 32) | lo);
+}
+
+__device__ __forceinline__ double read_lane(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(b), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), lane);
+  return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// Sum over the workgroup, waves added in order; `slots` holds one double a wave.
+// Lane rotations and lane reads instead of LDS shuffles: a tenth of their latency.
+__device__ __forceinline__ double block_sum(double s, double* slots, int wave, int lane, int nw) {
+  s += row_ror<8>(s);
+  s += row_ror<4>(s);
+  s += row_ror<2>(s);
+  s += row_ror<1>(s);
+  s = (read_lane(s, 0) + read_lane(s, 16)) + (read_lane(s, 32) + read_lane(s, 48));
+  if (nw == 1) return s;
   if (lane == 0) slots[wave] = s;
   __syncthreads();
   double t = slots[0];
@@ -83,9 +143,36 @@ __device__ __forceinline__ double block_sum(double s, double* slots, int wave, i
   return t;
 }
 
-// ROT: rotate and quantise; else only h and n are written.
-template <int BPW, bool ROT>
-__global__ __launch_bounds__(1024) void norm_rotate_kernel(NormArgs a) {
+// fmaxf over the wave of non-negative values, which order like their bits.
+__device__ __forceinline__ float wave_max(float m) {
+  uint32_t u = __float_as_uint(m);
+  u = max(u, row_ror<8>(u));
+  u = max(u, row_ror<4>(u));
+  u = max(u, row_ror<2>(u));
+  u = max(u, row_ror<1>(u));
+  const uint32_t a = max(__builtin_amdgcn_readlane(u, 0), __builtin_amdgcn_readlane(u, 16));
+  const uint32_t b = max(__builtin_amdgcn_readlane(u, 32), __builtin_amdgcn_readlane(u, 48));
+  return __uint_as_float(max(a, b));
+}
+
+// One lane's operands of a block that change with the token.
+struct TokenIn {
+  Row16 x, residual, gate;
+};
+
+// One lane's operands of a block that do not.
+struct Tables {
+  Row16 weight, post, gate;
+  uint4 sign;
+};
+
+// ROT: rotate and quantise; else only h and n are written.  BRANCH: any of
+// post_weight, gate, branch_scale and residual is there.
+// AHEAD (one block a wave): the next token's rows are loaded while this one is
+// computed.  WAVES: waves a SIMD that the registers have to leave room for.
+template <int BPW, bool ROT, bool BRANCH, bool AHEAD, int MAXT, int WAVES>
+__global__ __launch_bounds__(MAXT) __attribute__((amdgpu_waves_per_eu(WAVES)))
+void norm_rotate_kernel(NormArgs a) {
   extern __shared__ float wbuf_all[];  // ROT: nw x kWaveBufWords
   // two sets, alternated by token: a wave may write its slot of the next token
   // while another still reads this one's
@@ -96,134 +183,226 @@ __global__ __launch_bounds__(1024) void norm_rotate_kernel(NormArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x >> 6;
   const int K = a.K, nblocks = K / kBlock;
-  const bool branch = a.residual != nullptr || a.post_weight != nullptr || a.gate != nullptr || a.branch_scale != 1.0;
+  const bool post = BRANCH && a.post_weight != nullptr, gated = BRANCH && a.gate != nullptr;
+  const bool token_gate = gated && a.gate_stride != 0, residual = BRANCH && a.residual != nullptr;
   float* wb = wbuf_all + wave * kWaveBufWords;
+  static_assert(!AHEAD || BPW == 1, "one block a wave");
+
+  // a wave's block past the last re-reads it (no branch around loads) and is not used
+  const auto k_of = [&](int i) { return min(wave + i * nw, nblocks - 1) * kBlock; };
+  const auto load_x = [&](int64_t t, int i, TokenIn& in) { in.x = load16(a.x + static_cast<size_t>(t) * K + k_of(i), lane); };
+  const auto load_branch = [&](int64_t t, int i, TokenIn& in) {
+    if (residual) in.residual = load16(a.residual + static_cast<size_t>(t) * K + k_of(i), lane);
+    if (token_gate) in.gate = load16(a.gate + static_cast<size_t>(t) * a.gate_stride + k_of(i), lane);
+  };
+  const auto load_branch_tables = [&](int i, Tables& tab) {
+    if (post) tab.post = load16(a.post_weight + k_of(i), lane);
+    if (gated && !token_gate) tab.gate = load16(a.gate + k_of(i), lane);
+  };
+  const auto load_tables = [&](int i, Tables& tab) {
+    tab.weight = load16(a.weight + k_of(i), lane);
+    if (ROT) tab.sign = *reinterpret_cast<const uint4*>(a.sign + k_of(i) + 16 * lane);
+  };
+
+  int64_t t = blockIdx.x;  // the grid is at most M
+  TokenIn next = {};
+  if (AHEAD) {
+    load_x(t, 0, next);
+    load_branch(t, 0, next);
+  }
   int par = 0;
-  for (int64_t t = blockIdx.x; t < a.M; t += gridDim.x, par ^= 1) {
+  for (; t < a.M; t += gridDim.x, par ^= 1) {
     const size_t row = static_cast<size_t>(t) * K;
-    Row16 v[BPW];
+    TokenIn in[BPW];
+    Tables tab[BPW];
+    if (AHEAD) {
+      in[0] = next;
+      tab[0] = Tables{};
+      load_branch_tables(0, tab[0]);
+      const int64_t tn = std::min<int64_t>(t + gridDim.x, a.M - 1);
+      load_x(tn, 0, next);
+      load_branch(tn, 0, next);
+    } else {
 #pragma unroll
-    for (int i = 0; i < BPW; ++i) {
-      const int b = wave + i * nw;
-      v[i] = b < nblocks ? load16(a.x + row + b * kBlock + lane * 16) : Row16{};
+      for (int i = 0; i < BPW; ++i) {
+        in[i] = TokenIn{};
+        tab[i] = Tables{};
+        load_x(t, i, in[i]);
+        // two blocks' operands fit the registers ahead of the first sum, four do not
+        if (BPW <= 2) {
+          load_branch(t, i, in[i]);
+          load_branch_tables(i, tab[i]);
+        }
+      }
     }
-    if (branch) {
-      double inv = 1.0;
-      if (a.post_weight != nullptr) {
+    if (BRANCH) {
+      double factor = a.branch_scale;
+      if (post) {
         double s = 0.0;
 #pragma unroll
-        for (int i = 0; i < BPW; ++i) s += sum_squares(v[i]);
-        inv = 1.0 / sqrt(block_sum(s, post_slots[par], wave, lane, nw) / K + a.eps);
+        for (int i = 0; i < BPW; ++i)
+          if (wave + i * nw < nblocks) s += sum_squares(in[i].x);
+        const double mean = block_sum(s, post_slots[par], wave, lane, nw) * a.inv_k;
+        factor *= rsqrt(mean + a.eps);
+        if (mean > kLargeMean) {
+#pragma unroll
+          for (int i = 0; i < BPW; ++i) shrink(in[i].x);
+          factor *= kGrow;
+        }
       }
 #pragma unroll
       for (int i = 0; i < BPW; ++i) {
-        const int b = wave + i * nw;
-        if (b >= nblocks) continue;
-        if (BPW > 1) __builtin_amdgcn_sched_barrier(0);  // one block's operands at a time: no spills
-        const int k0 = b * kBlock + lane * 16;
-        Row16 pw{}, gt{}, rs{};
-        if (a.post_weight != nullptr) pw = load16(a.post_weight + k0);
-        if (a.gate != nullptr) gt = load16(a.gate + static_cast<size_t>(t) * a.gate_stride + k0);
-        if (a.residual != nullptr) rs = load16(a.residual + row + k0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          double lo = lo_f64(v[i].w[e]), hi = hi_f64(v[i].w[e]);
-          if (a.post_weight != nullptr) {
-            lo = lo * inv * lo_f64(pw.w[e]);
-            hi = hi * inv * hi_f64(pw.w[e]);
-          }
-          if (a.gate != nullptr) {
-            lo *= lo_f64(gt.w[e]);
-            hi *= hi_f64(gt.w[e]);
-          }
-          lo *= a.branch_scale;
-          hi *= a.branch_scale;
-          if (a.residual != nullptr) {
-            lo += lo_f64(rs.w[e]);
-            hi += hi_f64(rs.w[e]);
-          }
-          v[i].w[e] = pack_bf16(lo, hi);
+        if (BPW > 1) __builtin_amdgcn_sched_barrier(0);  // one block's fp64 values at a time: no spills
+        if (BPW > 2) {
+          load_branch(t, i, in[i]);
+          load_branch_tables(i, tab[i]);
         }
-        if (a.h != nullptr) store16(a.h + row + k0, v[i]);
+        const Row16& gate = token_gate ? in[i].gate : tab[i].gate;
+        Row16& v = in[i].x;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // eight elements, one uniform branch an operand (branches inside the
+          // element loop leave a wave waiting for each result in turn).  The product
+          // of two or three bf16 is exact in fp32.
+          float p[8];
+          double b[8];
+          const auto each = [&](const Row16& r, auto f) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t w = r.w[4 * half + e / 2];
+              f(e, __uint_as_float(e % 2 == 0 ? w << 16 : w & 0xFFFF0000u));
+            }
+          };
+          each(v, [&](int e, float x) { p[e] = x; });
+          if (post) each(tab[i].post, [&](int e, float w) { p[e] *= w; });
+          if (gated) each(gate, [&](int e, float g) { p[e] *= g; });
+          if (residual) {
+            each(in[i].residual, [&](int e, float x) { b[e] = __builtin_fma(static_cast<double>(p[e]), factor, static_cast<double>(x)); });
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] = static_cast<double>(p[e]) * factor;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v.w[4 * half + e] = pack_bf16(b[2 * e], b[2 * e + 1]);
+        }
+        if (a.h != nullptr && wave + i * nw < nblocks) store16(a.h + row + k_of(i), lane, v);
       }
+    }
+    if (BPW <= 2) {
+#pragma unroll
+      for (int i = 0; i < BPW; ++i) load_tables(i, tab[i]);
     }
     double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < BPW; ++i) s += sum_squares(v[i]);
-    const double inv = 1.0 / sqrt(block_sum(s, pre_slots[par], wave, lane, nw) / K + a.eps);
+    for (int i = 0; i < BPW; ++i)
+      if (wave + i * nw < nblocks) s += sum_squares(in[i].x);
+    const double mean = block_sum(s, pre_slots[par], wave, lane, nw) * a.inv_k;
+    double inv = rsqrt(mean + a.eps);
+    if (mean > kLargeMean) {
+#pragma unroll
+      for (int i = 0; i < BPW; ++i) shrink(in[i].x);
+      inv *= kGrow;
+    }
     float r[ROT ? BPW : 1][16];
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < BPW; ++i) {
-      const int b = wave + i * nw;
-      if (b >= nblocks) continue;
       if (BPW > 1) __builtin_amdgcn_sched_barrier(0);
-      const int k0 = b * kBlock + lane * 16;
-      const Row16 w = load16(a.weight + k0);
+      if (wave + i * nw >= nblocks) continue;
+      if (BPW > 2) load_tables(i, tab[i]);
+      Row16& v = in[i].x;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[i].w[e] = pack_bf16(lo_f64(v[i].w[e]) * inv * lo_f64(w.w[e]), hi_f64(v[i].w[e]) * inv * hi_f64(w.w[e]));
-      if (a.normed != nullptr) store16(a.normed + row + k0, v[i]);
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t x = v.w[e], w = tab[i].weight.w[e];
+        const float lo = __uint_as_float(x << 16) * __uint_as_float(w << 16);  // exact
+        const float hi = __uint_as_float(x & 0xFFFF0000u) * __uint_as_float(w & 0xFFFF0000u);
+        v.w[e] = pack_bf16(static_cast<double>(lo) * inv, static_cast<double>(hi) * inv);
+      }
+      if (a.normed != nullptr) store16(a.normed + row + k_of(i), lane, v);
       if constexpr (ROT) {
-        const uint4 sg = *reinterpret_cast<const uint4*>(a.sign + k0);
-        rot::BlockIn in = {{}, {}, {sg.x, sg.y, sg.z, sg.w}};
+        const Row16 c = consecutive(v, lane, wb);
+        const uint32_t sg[4] = {tab[i].sign.x, tab[i].sign.y, tab[i].sign.z, tab[i].sign.w};
+        rot::BlockIn b = {};  // signs applied here, two bf16 at a time
 #pragma unroll
-        for (int e = 0; e < 8; ++e) in.x[e] = v[i].w[e];
-        rot::rotate_loaded<false>(in, lane, wb, r[i]);
+        for (int e = 0; e < 8; ++e)
+          b.x[e] = c.w[e] ^ (__builtin_amdgcn_perm(0u, sg[e / 2], e % 2 == 0 ? 0x010C000Cu : 0x030C020Cu) & 0x80008000u);
+        rot::rotate_loaded<false, false>(b, lane, wb, r[i]);
 #pragma unroll
         for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(r[i][e]));
       }
     }
     if constexpr (ROT) {
-#pragma unroll
-      for (int m = 32; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
-      if (lane == 0) max_slots[par][wave] = amax;
-      __syncthreads();
-      float tmax = max_slots[par][0];
-      for (int w = 1; w < nw; ++w) tmax = fmaxf(tmax, max_slots[par][w]);
-      const rot::TokenQuant tq = rot::token_quant(tmax);
-      if (threadIdx.x == 0) a.a_scale[t] = tq.scale;
-#pragma unroll
-      for (int i = 0; i < BPW; ++i) {
-        const int b = wave + i * nw;
-        if (b >= nblocks) continue;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint32_t*>(a.x_i8 + row + b * kBlock + 256 * c + 4 * lane) = rot::quant_run(r[i], c, tq);
+      float tmax = wave_max(amax);
+      if (nw > 1) {
+        if (lane == 0) max_slots[par][wave] = tmax;
+        __syncthreads();
+        for (int w = 0; w < nw; ++w) tmax = fmaxf(tmax, max_slots[par][w]);
       }
+      const rot::TokenQuant tq = rot::token_quant_unscaled(tmax);
+      if (threadIdx.x == 0) a.a_scale[t] = tq.scale;
+      const auto store_all = [&](auto quotient) {
+#pragma unroll
+        for (int i = 0; i < BPW; ++i) {
+          const int b = wave + i * nw;
+          if (b >= nblocks) continue;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) word |= rot::quant_byte(quotient(r[i][4 * c + d])) << (8 * d);
+            *reinterpret_cast<uint32_t*>(a.x_i8 + row + b * kBlock + 256 * c + 4 * lane) = word;
+          }
+        }
+      };
+      // the test is hoisted out of the element loop (one branch per token)
+      if (tq.markstein)
+        store_all([&](float w) { return rot::quotient_markstein(w, tq); });
+      else
+        store_all([&](float w) { return w / tq.div; });
     }
   }
 }
 
-template <int BPW, bool ROT>
-hipError_t launch_bpw(const NormArgs& a, hipStream_t stream) {
+template <int BPW, bool ROT, bool BRANCH, bool AHEAD, int MAXT, int WAVES>
+hipError_t launch_form(const NormArgs& a, const DeviceInfo& dev, hipStream_t stream) {
   const int nblocks = a.K / kBlock;
   const int nw = (nblocks + BPW - 1) / BPW;
+  if (nw > kMaxNormWaves || 64 * nw > MAXT) return hipErrorInvalidValue;
   const size_t lds = ROT ? static_cast<size_t>(nw) * kWaveBufWords * sizeof(float) : 0;
   if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(norm_rotate_kernel<BPW, ROT>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(norm_rotate_kernel<BPW, ROT, BRANCH, AHEAD, MAXT, WAVES>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
     if (e != hipSuccess) return e;
   }
-  // one workgroup a token, up to the grid limit; past it workgroups take several
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.M, 1 << 20));
-  hipLaunchKernelGGL((norm_rotate_kernel<BPW, ROT>), dim3(grid), dim3(64 * nw), lds, stream, a);
+  // as many workgroups as are resident at once, so that all of them take the same
+  // number of tokens, one more at most
+  int per_cu = 1;
+  const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(
+      &per_cu, norm_rotate_kernel<BPW, ROT, BRANCH, AHEAD, MAXT, WAVES>, 64 * nw, lds);
+  if (e != hipSuccess) return e;
+  const int64_t resident = static_cast<int64_t>(std::max(1, dev.cu_count)) * std::max(1, per_cu);
+  hipLaunchKernelGGL((norm_rotate_kernel<BPW, ROT, BRANCH, AHEAD, MAXT, WAVES>), dim3(static_cast<unsigned>(std::min(a.M, resident))),
+                     dim3(64 * nw), lds, stream, a);
   return hipGetLastError();
 }
 
-template <bool ROT>
-hipError_t launch_rot(const NormArgs& a, hipStream_t stream) {
+template <bool ROT, bool BRANCH>
+hipError_t launch_blocks(const NormArgs& a, const DeviceInfo& dev, hipStream_t stream) {
   const int nblocks = a.K / kBlock;  // 1 .. 64 (validated by the caller)
-  if (nblocks <= 16) return launch_bpw<1, ROT>(a, stream);
-  if (nblocks <= 32) return launch_bpw<2, ROT>(a, stream);
-  return launch_bpw<4, ROT>(a, stream);
+  if (nblocks <= 8) return launch_form<1, ROT, BRANCH, true, 512, 4>(a, dev, stream);
+  if (nblocks <= 24) return launch_form<2, ROT, BRANCH, false, 768, 3>(a, dev, stream);
+  if (nblocks <= 48) return launch_form<4, ROT, BRANCH, false, 768, 3>(a, dev, stream);
+  return launch_form<4, ROT, BRANCH, false, 1024, 4>(a, dev, stream);
 }
 
 }  // namespace
 
-hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t stream) {
+hipError_t launch_norm_rotate(NormArgs a, const DeviceInfo& dev, hipStream_t stream) {
   if (a.M == 0) return hipSuccess;
-  return a.sign != nullptr ? launch_rot<true>(a, stream) : launch_rot<false>(a, stream);
+  a.inv_k = 1.0 / a.K;
+  const bool branch = a.residual != nullptr || a.post_weight != nullptr || a.gate != nullptr || a.branch_scale != 1.0;
+  if (a.sign != nullptr) return branch ? launch_blocks<true, true>(a, dev, stream) : launch_blocks<true, false>(a, dev, stream);
+  return branch ? launch_blocks<false, true>(a, dev, stream) : launch_blocks<false, false>(a, dev, stream);
 }
 
 }  // namespace twl

@@ -152,8 +152,9 @@ __device__ __forceinline__ BlockIn load_block_rt(const uint16_t* __restrict__ xr
 // The rotation of one loaded block by one wave (with SILU the rotated input
 // is bf16(SiLU(gate) * up)); wb is this wave's transpose buffer
 // (kWaveBufWords floats).  On return w holds (1/32) H1024 (sign . x) of the
-// block in layout 2.
-template <bool SILU>
+// block in layout 2.  SCALED = false leaves out the factor 1/32 (a power of two,
+// which commutes with every rounding that follows; see token_quant_unscaled).
+template <bool SILU, bool SCALED = true>
 __device__ __forceinline__ void rotate_loaded(const BlockIn& in, int lane, float* wb, float (&w)[16]) {
   // layout-1 lane bits: e[9:8] = lane >> 4, e[3:0] = lane & 15
   const int l1_hi = lane >> 4, l1_lo = lane & 15;
@@ -200,8 +201,10 @@ __device__ __forceinline__ void rotate_loaded(const BlockIn& in, int lane, float
   }
 #pragma unroll
   for (int sb = 2; sb < 4; ++sb) stage_in_lane(w, sb);  // h = 256, 512
+  if (SCALED) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] *= 0.03125f;  // orthonormal 1/sqrt(1024): exact power of two
+    for (int e = 0; e < 16; ++e) w[e] *= 0.03125f;  // orthonormal 1/sqrt(1024): exact power of two
+  }
 }
 
 // Block b of one token, loaded and rotated by one wave (see load_block and
@@ -237,6 +240,16 @@ __device__ __forceinline__ TokenQuant token_quant(float absmax) {
   t.div = t.scale > 0.0f ? t.scale : 1.0f;
   t.markstein = t.div >= 0x1p-64f;
   t.inv = 1.0f / t.div;  // IEEE division
+  return t;
+}
+
+// The quantiser for values 32 r of rotate_loaded<., false>, given their absmax: the
+// scale of r itself, and divisor and reciprocal for 32 r.  Every quotient is that of
+// r and the scale to the bit (multiplying by 32 rounds nothing).
+__device__ __forceinline__ TokenQuant token_quant_unscaled(float absmax32) {
+  TokenQuant t = token_quant(absmax32 * 0.03125f);
+  t.div *= 32.0f;
+  t.inv *= 0.03125f;
   return t;
 }
 

@@ -133,10 +133,11 @@ struct NormArgs {
   int8_t* x_i8;
   float* a_scale;
   double branch_scale, eps;
+  double inv_k;  // 1 / K, set by the launcher
   int64_t M, gate_stride;
   int K;
 };
-hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t stream);
+hipError_t launch_norm_rotate(NormArgs a, const DeviceInfo& dev, hipStream_t stream);
 
 // lora_add (include/twl.h).  The caller sets the operands and sizes; the
 // launcher plans the rest.  `part` holds lora_workspace_bytes.

@@ -7,7 +7,7 @@
 //
 // Two kernels, both on v_mfma_f32_16x16x32_bf16 with the adapter's rows as the
 // first operand and 16 tokens as the second, so that a lane's results are
-// consecutive ranks (or consecutive n) of one token:
+// consecutive ranks (or n) of one token:
 //   shrink  a workgroup takes 16 consecutive tokens and a slice of K, its waves
 //           split the slice; their sums meet in LDS (in wave order) and the slice's
 //           sum goes to the workspace, fp32 [slices][M][R].
@@ -31,10 +31,11 @@ namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kShrinkWaves = 8;
 constexpr int kExpandWaves = 4;
-constexpr int kChunk = 32 * kExpandWaves;  // n of one round of an expand workgroup
+constexpr int kChunk = 64 * kExpandWaves;  // n of one round of an expand workgroup
 
 __device__ __forceinline__ v8bf load8(const uint16_t* p) { return *reinterpret_cast<const v8bf*>(p); }
 
@@ -60,171 +61,301 @@ struct Passes {
   }
 };
 
-// Workgroup (tile, slice, p): passes p, p + passes, ... of 16 tokens over one
+// Workgroups are dispatched to the XCDs in turn: work item of workgroup `bid` such
+// that each XCD gets a contiguous range of the items, whose neighbours share an
+// adapter's rows in its L2.
+__device__ __forceinline__ int xcd_item(int bid, int total) {
+  constexpr int kXcds = 8;
+  const int per = total / kXcds, rem = total % kXcds, xcd = bid % kXcds;
+  return xcd * per + min(xcd, rem) + bid / kXcds;
+}
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+// two fp32 -> two bf16, to nearest even (v_cvt_pk_bf16_f32)
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const v2f f = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, v2bf));
+}
+
+// LDS operations of one wave execute in order; this only keeps the compiler from
+// moving the reads of other lanes' data above the writes, or the next writes above
+// these reads.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Work item (slice, tile, p): passes p, p + passes, ... of 16 TS tokens over one
 // slice of K.  RT: 16-row fragments of the rank.
-template <int RT>
+//
+// A load straight into the operand's layout (lane = 16 bytes of one of 16 rows)
+// touches 64 cache lines an instruction, and the address unit bounds the kernel
+// (4096 tokens of 5120, rank 64: 54 us).  So a wave loads 64 k of its rows with 8
+// lanes a row and 8 rows an instruction, and turns them over in LDS of its own
+// (16-byte units swizzled by row, no bank conflicts): no barrier before the sums
+// meet.
+template <int RT, int TS>
 __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs a) {
-  constexpr int kStride = 16 * RT + 4;  // floats of a token's row, padded
-  __shared__ __attribute__((aligned(16))) float red[kShrinkWaves][16 * kStride];
+  constexpr int TM = 16 * TS;
+  constexpr int kStride = 16 * RT + 4;  // floats of a token's row of sums, padded
+  constexpr int G = 2 * (TS + RT);      // groups of 8 rows: x, then A
+  constexpr int U = G <= 6 ? 2 : 1;     // 64-k units loaded together
+  constexpr int kStage = U * G * 1024, kSums = TM * kStride * 4;
+  __shared__ __attribute__((aligned(16))) char lds[kShrinkWaves * (kStage > kSums ? kStage : kSums)];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j = lane & 15, q = lane >> 4;
-  const int tile = blockIdx.x % a.shrink_tiles;
-  const int rest = blockIdx.x / a.shrink_tiles;
-  const int p = rest % a.shrink_passes, slice = rest / a.shrink_passes;
-  const int64_t t0 = static_cast<int64_t>(tile) * 16;
+  const uint32_t item = xcd_item(blockIdx.x, gridDim.x), first = item / a.shrink_passes;
+  const int p = item - first * a.shrink_passes;
+  const int slice = first / a.shrink_tiles, tile = first - slice * a.shrink_tiles;
+  const int64_t t0 = static_cast<int64_t>(tile) * TM;
   const int K = a.K, R = a.R;
-  // this wave's 32-k steps
-  const int steps = K / 32, parts = a.slices * kShrinkWaves, part = slice * kShrinkWaves + wave;
-  const int s0 = static_cast<int>(static_cast<int64_t>(steps) * part / parts);
-  const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (part + 1) / parts);
-  const uint16_t* xr = a.x + std::min<int64_t>(t0 + j, a.M - 1) * K + 8 * q;
+  // this wave's 64-k units
+  const uint32_t units = K / 64, parts = a.slices * kShrinkWaves, part = slice * kShrinkWaves + wave;
+  const int u0 = static_cast<int>(units * part / parts), u1 = static_cast<int>(units * (part + 1) / parts);  // <= 2^10 parts
+  char* stage = lds + wave * kStage;
+  float* sums = reinterpret_cast<float*>(lds);  // [wave][token][rank], when the staging is done
 
-  Passes passes(a.ids, t0, 16, a.M, a.n, lane);
+  const int r8 = lane >> 3, c8 = lane & 7;  // row of a group and 16-byte unit of this lane's loads
+  const char* xb = reinterpret_cast<const char*>(a.x + static_cast<size_t>(t0) * K);
+  const int rows = static_cast<int>(std::min<int64_t>(TM, a.M - t0));
+  uint32_t off[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int r = g < 2 * TS ? min(8 * g + r8, rows - 1) : min(8 * (g - 2 * TS) + r8, R - 1);
+    off[g] = static_cast<uint32_t>(r) * static_cast<uint32_t>(2 * K) + 16 * c8;
+  }
+  const int put = r8 * 128 + 16 * (c8 ^ r8);
+  const auto get = [&](int u, int frag, int s) {  // fragment frag (x, then A), k step s of unit u
+    const int at = (u * G + 2 * frag + (j >> 3)) * 1024 + (j & 7) * 128 + 16 * ((4 * s + q) ^ (j & 7));
+    return *reinterpret_cast<const v8bf*>(stage + at);
+  };
+
+  Passes passes(a.ids, t0, TM, a.M, a.n, lane);
   int adapter;
   uint64_t tokens;
-  for (int i = 0; passes.next(adapter, tokens); ++i) {
-    if (i % a.shrink_passes != p) continue;
-    const uint16_t* ar[RT];
+  for (int skip = p; passes.next(adapter, tokens); --skip) {
+    if (skip != 0) continue;
+    skip = a.shrink_passes;
+    const char* ab = reinterpret_cast<const char*>(a.a + static_cast<size_t>(adapter) * R * K);
+    v4f acc[TS][RT];
 #pragma unroll
-    for (int f = 0; f < RT; ++f)
-      ar[f] = a.a + (static_cast<size_t>(adapter) * R + min(16 * f + j, R - 1)) * K + 8 * q;
-    v4f acc[RT];
+    for (int h = 0; h < TS; ++h)
 #pragma unroll
-    for (int f = 0; f < RT; ++f) acc[f] = v4f{0};
-    const auto run = [&](int s, auto count) {  // `count` steps from s, all their loads in flight together
-      constexpr int U = decltype(count)::value;
-      v8bf xv[U], av[U][RT];
+      for (int f = 0; f < RT; ++f) acc[h][f] = v4f{0};
+    v4u raw[U][G];
+    const auto load = [&](int u) {  // units past the last re-read it and are not multiplied
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        xv[u] = load8(xr + 32 * (s + u));
+      for (int v = 0; v < U; ++v)
 #pragma unroll
-        for (int f = 0; f < RT; ++f) av[u][f] = load8(ar[f] + 32 * (s + u));
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int f = 0; f < RT; ++f)
-          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[u][f], xv[u], acc[f], 0, 0, 0);
+        for (int g = 0; g < G; ++g)
+          raw[v][g] = *reinterpret_cast<const v4u*>((g < 2 * TS ? xb : ab) + off[g] + 128 * min(u + v, u1 - 1));
     };
-    constexpr int U = RT <= 2 ? 8 : RT == 4 ? 4 : 2;
-    int s = s0;
-    for (; s + U <= s1; s += U) run(s, std::integral_constant<int, U>());
-    for (; s < s1; ++s) run(s, std::integral_constant<int, 1>());
-    // lane (j, q) holds ranks 16 f + 4 q .. + 3 of token j
-    __syncthreads();  // the previous pass has been read
+    if (u0 < u1) load(u0);
+    for (int u = u0; u < u1; u += U) {
+      wave_lds_sync();  // the previous units have been read
 #pragma unroll
-    for (int f = 0; f < RT; ++f) *reinterpret_cast<v4f*>(&red[wave][j * kStride + 16 * f + 4 * q]) = acc[f];
+      for (int v = 0; v < U; ++v)
+#pragma unroll
+        for (int g = 0; g < G; ++g) *reinterpret_cast<v4u*>(stage + (v * G + g) * 1024 + put) = raw[v][g];
+      if (u + U < u1) load(u + U);
+      wave_lds_sync();
+#pragma unroll
+      for (int v = 0; v < U; ++v) {
+        if (u + v >= u1) break;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          v8bf xv[TS];
+#pragma unroll
+          for (int h = 0; h < TS; ++h) xv[h] = get(v, h, s);
+#pragma unroll
+          for (int f = 0; f < RT; ++f) {
+            const v8bf av = get(v, TS + f, s);
+#pragma unroll
+            for (int h = 0; h < TS; ++h) acc[h][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xv[h], acc[h][f], 0, 0, 0);
+          }
+        }
+      }
+    }
+    // lane (j, q) holds ranks 16 f + 4 q .. + 3 of token 16 h + j
+    __syncthreads();  // every wave is past its staging
+#pragma unroll
+    for (int h = 0; h < TS; ++h)
+#pragma unroll
+      for (int f = 0; f < RT; ++f)
+        *reinterpret_cast<v4f*>(sums + (wave * TM + 16 * h + j) * kStride + 16 * f + 4 * q) = acc[h][f];
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * (R / 4); e += 64 * kShrinkWaves) {
+    for (int e = threadIdx.x; e < TM * (R / 4); e += 64 * kShrinkWaves) {
       const int tok = e / (R / 4), r = 4 * (e % (R / 4));
       if (!((tokens >> tok) & 1)) continue;
-      v4f sum = *reinterpret_cast<const v4f*>(&red[0][tok * kStride + r]);
+      v4f sum = *reinterpret_cast<const v4f*>(sums + tok * kStride + r);
 #pragma unroll
-      for (int w = 1; w < kShrinkWaves; ++w) sum += *reinterpret_cast<const v4f*>(&red[w][tok * kStride + r]);
+      for (int w = 1; w < kShrinkWaves; ++w) sum += *reinterpret_cast<const v4f*>(sums + (w * TM + tok) * kStride + r);
       *reinterpret_cast<v4f*>(a.part + (static_cast<size_t>(slice) * a.M + t0 + tok) * R + r) = sum;
+    }
+    __syncthreads();  // the sums have been read: the next pass stages over them
+  }
+}
+
+// One wave's 16 tokens x 64 n of y, in y's type, where rows are 16-byte aligned: 8
+// (fp32: 16) lanes a token, 16 bytes each.
+template <bool BF16>
+struct Out {
+  static constexpr int kItems = BF16 ? 2 : 4;  // instructions
+  static constexpr int kEach = BF16 ? 8 : 4;   // elements of 16 bytes
+  static constexpr int kLanes = 64 / kEach;    // lanes a token
+  v4u raw[kItems];
+
+  static __device__ __forceinline__ int token(int i, int lane) { return (64 * i + lane) / kLanes; }
+  static __device__ __forceinline__ int column(int lane) { return kEach * (lane % kLanes); }
+
+  __device__ __forceinline__ void load(int i, const void* y, size_t at) {
+    raw[i] = *reinterpret_cast<const v4u*>(static_cast<const char*>(y) + at * (BF16 ? 2 : 4));
+  }
+
+  // adds d[0 ..] to item i and stores it
+  __device__ __forceinline__ void finish(int i, void* out, size_t at, const float* d) {
+    const v4u r = raw[i];
+    v4u w;
+    if constexpr (BF16) {
+      const v4f lo = *reinterpret_cast<const v4f*>(d), hi = *reinterpret_cast<const v4f*>(d + 4);
+      const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack_bf16(__uint_as_float(r[e] << 16) + v[2 * e], __uint_as_float(r[e] & 0xFFFF0000u) + v[2 * e + 1]);
+    } else {
+      const v4f v = *reinterpret_cast<const v4f*>(d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(r[e]) + v[e]);
+    }
+    *reinterpret_cast<v4u*>(static_cast<char*>(out) + at * (BF16 ? 2 : 4)) = w;
+  }
+};
+
+// The same for rows of any alignment: out = y + d (d in LDS, a row of kStride floats
+// a token; null: nothing) of the tokens of `tokens`, one token an instruction, lane =
+// one n.
+template <bool BF16, int kStride>
+__device__ __forceinline__ void finish_unaligned(const void* y, void* out, const float* d, uint64_t tokens, size_t row0,
+                                                 int N, int nb, int lane) {
+  if (nb + lane >= N) return;
+  const size_t at0 = row0 * N + nb + lane;
+#pragma unroll 4
+  for (int t = 0; t < 16; ++t) {
+    if (((tokens >> t) & 1) == 0) continue;
+    const size_t at = at0 + static_cast<size_t>(t) * N;
+    const float add = d != nullptr ? d[t * kStride + lane] : 0.0f;
+    if constexpr (BF16) {
+      const float v = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(y)[at]) << 16);
+      static_cast<uint16_t*>(out)[at] = static_cast<uint16_t>(pack_bf16(v + add, 0.0f));
+    } else {
+      static_cast<float*>(out)[at] = static_cast<const float*>(y)[at] + add;
     }
   }
 }
 
-// 8 consecutive outputs of one token, n0 .. n0 + 7.  VEC: rows are 16-byte aligned
-// (N % 8 == 0), so the eight are inside the row together.
-template <bool BF16, bool VEC>
-struct Out8 {
-  float v[8];
-
-  __device__ __forceinline__ void load(const void* y, size_t row, int n0, int N) {
-    if constexpr (VEC) {
-      if (n0 >= N) return;
-      if constexpr (BF16) {
-        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(y) + row + n0);
-        const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[2 * e] = __uint_as_float(d[e] << 16);
-          v[2 * e + 1] = __uint_as_float(d[e] & 0xFFFF0000u);
-        }
-      } else {
-        const v4f lo = *reinterpret_cast<const v4f*>(static_cast<const float*>(y) + row + n0);
-        const v4f hi = *reinterpret_cast<const v4f*>(static_cast<const float*>(y) + row + n0 + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = lo[e];
-          v[4 + e] = hi[e];
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (n0 + e < N)
-          v[e] = BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(y)[row + n0 + e]) << 16)
-                      : static_cast<const float*>(y)[row + n0 + e];
-    }
-  }
-
-  __device__ __forceinline__ void store(void* out, size_t row, int n0, int N) const {
-    if constexpr (VEC) {
-      if (n0 >= N) return;
-      if constexpr (BF16) {
-        uint32_t d[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          d[e] = f32_to_bf16_rne(v[2 * e]) | (static_cast<uint32_t>(f32_to_bf16_rne(v[2 * e + 1])) << 16);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row + n0) = make_uint4(d[0], d[1], d[2], d[3]);
-      } else {
-        *reinterpret_cast<v4f*>(static_cast<float*>(out) + row + n0) = v4f{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<v4f*>(static_cast<float*>(out) + row + n0 + 4) = v4f{v[4], v[5], v[6], v[7]};
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (n0 + e < N) {
-          if (BF16)
-            static_cast<uint16_t*>(out)[row + n0 + e] = f32_to_bf16_rne(v[e]);
-          else
-            static_cast<float*>(out)[row + n0 + e] = v[e];
-        }
-    }
-  }
-};
-
-// Workgroup (chunk, tile, p): passes p, p + passes, ... of 16 TT tokens over
-// `expand_rounds` ranges of kChunk n.  RS: 32-rank steps.
+// Work item (chunk, tile, p): passes p, p + passes, ... of 16 TT tokens over
+// `expand_rounds` ranges of kChunk n, 64 n a wave.  RS: 32-rank steps.
+//
+// As in the shrink kernel nothing is read or written in the matrix layout, whose
+// lanes lie a row of y apart (measured with it: 145 us for 4096 tokens of rank 64
+// on 17408, bf16): B's 64 rows are one piece of memory, copied to the wave's LDS
+// in order, and the products go through LDS to where y's 16-byte pieces are.  B and
+// y of the next range are on their way while this one is computed.
 template <int TT, int RS, bool BF16, bool VEC>
 __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs a) {
+  using Y = Out<BF16>;
   constexpr int TM = 16 * TT, TERMS = BF16 ? 2 : 3;
-  constexpr int kStride = 32 * RS + 8;  // bf16 of a token's row, padded
+  // fragments of tokens whose y is loaded ahead: 8 KB a wave in flight
+  constexpr int AHEAD = BF16 ? TT : (TT < 2 ? TT : 2);
+  constexpr int kStride = 32 * RS + 8;  // bf16 of a row of v or B, padded
+  constexpr int kOutStride = 64 + 4;    // floats of a token's products, padded
+  constexpr int BL = 4 * RS;            // 16-byte loads a lane for 64 rows of B of full rank
   __shared__ __attribute__((aligned(16))) uint16_t vt[TERMS][TM * kStride];
+  __shared__ __attribute__((aligned(16))) uint16_t b_lds[kExpandWaves][64 * kStride];
+  __shared__ __attribute__((aligned(16))) float d_lds[kExpandWaves][16 * kOutStride];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j = lane & 15, q = lane >> 4;
-  const int chunk = blockIdx.x % a.expand_chunks;
-  const int rest = blockIdx.x / a.expand_chunks;
-  const int p = rest % a.expand_passes, tile = rest / a.expand_passes;
+  const uint32_t item = xcd_item(blockIdx.x, gridDim.x), first = item / a.expand_passes;
+  const int p = item - first * a.expand_passes;
+  const int chunk = first / a.expand_tiles, tile = first - chunk * a.expand_tiles;
   const int64_t t0 = static_cast<int64_t>(tile) * TM;
   const int N = a.N, R = a.R;
-  const int n_lo = chunk * a.expand_rounds * kChunk + 32 * wave;
+  const int n_lo = chunk * a.expand_rounds * kChunk + 64 * wave;
   const int n_hi = min(N, (chunk + 1) * a.expand_rounds * kChunk);
+  uint16_t* bw = b_lds[wave];
+  float* dw = d_lds[wave];
+  const int col = Y::column(lane);
+  const auto row = [&](int tt, int i) { return static_cast<size_t>(t0 + 16 * tt + Y::token(i, lane)) * N; };
+  const auto has = [&](uint64_t tokens, int tt, int i) { return ((tokens >> (16 * tt + Y::token(i, lane))) & 1) != 0; };
 
   Passes passes(a.ids, t0, TM, a.M, a.n, lane);
   if (a.out != a.y && p == 0) {
     // tokens without an adapter
     const uint64_t tokens = __ballot(passes.id < 0 && lane < TM && t0 + lane < a.M);
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
-      if ((tokens >> (16 * tt + j)) & 1) {
-        const size_t row = static_cast<size_t>(t0 + 16 * tt + j) * N;
-        for (int nb = n_lo; nb < n_hi; nb += kChunk) {
-          Out8<BF16, VEC> o;
-          o.load(a.y, row, nb + 8 * q, N);
-          o.store(a.out, row, nb + 8 * q, N);
+    for (int tt = 0; tt < TT; ++tt) {
+      if (((tokens >> (16 * tt)) & 0xFFFF) == 0) continue;
+      for (int nb = n_lo; nb < n_hi; nb += kChunk) {
+        if constexpr (VEC) {
+#pragma unroll
+          for (int i = 0; i < Y::kItems; ++i)
+            if (has(tokens, tt, i) && nb + col < N) {
+              const size_t at = (row(tt, i) + nb + col) * (BF16 ? 2 : 4);
+              *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + at) =
+                  *reinterpret_cast<const uint4*>(static_cast<const char*>(a.y) + at);
+            }
+        } else {
+          finish_unaligned<BF16, kOutStride>(a.y, a.out, nullptr, tokens >> (16 * tt), static_cast<size_t>(t0 + 16 * tt), N,
+                                             nb, lane);
         }
       }
+    }
+  }
+  // the 16-byte pieces of 64 rows of B, R / 8 a row: piece 64 l + lane for l < R / 8
+  const int pieces = R / 8;
+  int b_at[BL];  // where it goes in bw
+#pragma unroll
+  for (int l = 0; l < BL; ++l) {
+    const int c = 64 * l + lane;
+    b_at[l] = (c / pieces) * kStride + 8 * (c % pieces);
+  }
+  if (pieces < BL) {  // the columns past the rank stay zero: v is zero there, B has to be finite
+    for (int e = lane; e < 64 * kStride / 8; e += 64) *reinterpret_cast<uint4*>(bw + 8 * e) = make_uint4(0, 0, 0, 0);
+    wave_lds_sync();
   }
   int adapter;
   uint64_t tokens;
-  for (int i = 0; passes.next(adapter, tokens); ++i) {
-    if (i % a.expand_passes != p) continue;
+  for (int skip = p; passes.next(adapter, tokens); --skip) {
+    if (skip != 0) continue;
+    skip = a.expand_passes;
+    const uint16_t* ba = a.b + static_cast<size_t>(adapter) * N * R;
+    v4u braw[BL];
+    Y y[AHEAD];
+    const auto load_b = [&](int nb) {
+      // pieces past the 64 rows (a rank below 32 RS) are not used; those past the
+      // adapter's end re-read its last one
+      const size_t first = static_cast<size_t>(nb) * R, last = static_cast<size_t>(N) * R - 8;
+#pragma unroll
+      for (int l = 0; l < BL; ++l)
+        braw[l] = *reinterpret_cast<const v4u*>(ba + std::min<size_t>(first + 8 * (64 * l + lane), last));
+    };
+    const auto load_y = [&](int tt, int nb) {
+#pragma unroll
+      for (int i = 0; i < Y::kItems; ++i)
+        if (has(tokens, tt, i) && nb + col < N) y[tt % AHEAD].load(i, a.y, row(tt, i) + nb + col);
+    };
+    if (n_lo < n_hi) {
+      load_b(n_lo);
+      if (VEC) {
+#pragma unroll
+        for (int tt = 0; tt < AHEAD; ++tt) load_y(tt, n_lo);
+      }
+    }
     const float scale = a.scale[adapter];
     __syncthreads();  // the previous pass has been read
     for (int e = threadIdx.x; e < TM * (32 * RS / 4); e += 64 * kExpandWaves) {
@@ -232,53 +363,68 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
       v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
       if (r < R && ((tokens >> tok) & 1)) {
         const float* src = a.part + static_cast<size_t>(t0 + tok) * R + r;
-        for (int s = 0; s < a.slices; ++s) v += *reinterpret_cast<const v4f*>(src + static_cast<size_t>(s) * a.M * R);
+        const size_t next = static_cast<size_t>(a.M) * R;
+        for (int s = 0; s < a.slices; s += 8) {  // eight loads in flight, added in order
+          v4f part[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) part[u] = *reinterpret_cast<const v4f*>(src + min(s + u, a.slices - 1) * next);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (s + u < a.slices) v += part[u];
+        }
         v *= scale;
       }
 #pragma unroll
       for (int term = 0; term < TERMS; ++term) {
-        uint16_t b[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          b[c] = f32_to_bf16_rne(v[c]);
-          v[c] -= __uint_as_float(static_cast<uint32_t>(b[c]) << 16);
-        }
-        *reinterpret_cast<uint2*>(&vt[term][tok * kStride + r]) =
-            make_uint2(b[0] | (static_cast<uint32_t>(b[1]) << 16), b[2] | (static_cast<uint32_t>(b[3]) << 16));
+        const uint2 b = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        v -= v4f{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u), __uint_as_float(b.y << 16),
+                 __uint_as_float(b.y & 0xFFFF0000u)};
+        *reinterpret_cast<uint2*>(&vt[term][tok * kStride + r]) = b;
       }
     }
     __syncthreads();
     for (int nb = n_lo; nb < n_hi; nb += kChunk) {
-      // fragment f row i of the first operand is n = nb + 8 (i / 4) + 4 f + i % 4, so
-      // that lane (j, q) ends up with n = nb + 8 q .. + 7 of token j
-      v8bf w[2][RS];
+      wave_lds_sync();  // the previous range's B has been read
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int n = min(nb + 8 * (j >> 2) + 4 * f + (j & 3), N - 1);
-        const uint16_t* br = a.b + (static_cast<size_t>(adapter) * N + n) * R;
+      for (int l = 0; l < BL; ++l)
+        if (l < pieces) *reinterpret_cast<v4u*>(bw + b_at[l]) = braw[l];
+      const bool more = nb + kChunk < n_hi;
+      if (more) load_b(nb + kChunk);
+      wave_lds_sync();
+      v8bf w[4][RS];
 #pragma unroll
-        for (int s = 0; s < RS; ++s) w[f][s] = load8(br + min(32 * s + 8 * q, R - 8));
-      }
+      for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int s = 0; s < RS; ++s) w[f][s] = load8(bw + (16 * f + j) * kStride + 32 * s + 8 * q);
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) {
-        if (((tokens >> (16 * tt)) & 0xFFFF) == 0) continue;
-        const bool mine = (tokens >> (16 * tt + j)) & 1;
-        const size_t row = static_cast<size_t>(t0 + 16 * tt + j) * N;
-        Out8<BF16, VEC> o;
-        if (mine) o.load(a.y, row, nb + 8 * q, N);
-        v4f acc[2] = {v4f{0}, v4f{0}};
+        if (!VEC && ((tokens >> (16 * tt)) & 0xFFFF) == 0) continue;  // VEC: keeps the loads ahead in step
+        v4f acc[4] = {v4f{0}, v4f{0}, v4f{0}, v4f{0}};
 #pragma unroll
         for (int s = 0; s < RS; ++s)
 #pragma unroll
           for (int term = 0; term < TERMS; ++term) {
             const v8bf v = load8(&vt[term][(16 * tt + j) * kStride + 32 * s + 8 * q]);
 #pragma unroll
-            for (int f = 0; f < 2; ++f) acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[f][s], v, acc[f], 0, 0, 0);
+            for (int f = 0; f < 4; ++f) acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[f][s], v, acc[f], 0, 0, 0);
           }
-        if (mine) {
+        // lane (j, q) holds n = nb + 16 f + 4 q .. + 3 of token j
+        wave_lds_sync();  // the previous products have been read
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o.v[e] += acc[e >> 2][e & 3];
-          o.store(a.out, row, nb + 8 * q, N);
+        for (int f = 0; f < 4; ++f) *reinterpret_cast<v4f*>(dw + j * kOutStride + 16 * f + 4 * q) = acc[f];
+        wave_lds_sync();
+        if constexpr (VEC) {
+#pragma unroll
+          for (int i = 0; i < Y::kItems; ++i)
+            if (has(tokens, tt, i) && nb + col < N)
+              y[tt % AHEAD].finish(i, a.out, row(tt, i) + nb + col, dw + Y::token(i, lane) * kOutStride + col);
+        } else {
+          finish_unaligned<BF16, kOutStride>(a.y, a.out, dw, tokens >> (16 * tt), static_cast<size_t>(t0 + 16 * tt), N, nb,
+                                             lane);
+        }
+        if constexpr (VEC) {
+          if (tt + AHEAD < TT) load_y(tt + AHEAD, nb);
+          else if (more) load_y(tt + AHEAD - TT, nb + kChunk);
         }
       }
     }
@@ -288,7 +434,7 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
 template <int TT, int RS>
 hipError_t launch_expand(const LoraArgs& a, bool bf16, unsigned grid, hipStream_t stream) {
   const dim3 g(grid), b(64 * kExpandWaves);
-  const bool vec = a.N % 8 == 0;
+  const bool vec = a.N % (bf16 ? 8 : 4) == 0;  // rows of y 16-byte aligned
   if (bf16 && vec) hipLaunchKernelGGL((lora_expand_kernel<TT, RS, true, true>), g, b, 0, stream, a);
   else if (bf16) hipLaunchKernelGGL((lora_expand_kernel<TT, RS, true, false>), g, b, 0, stream, a);
   else if (vec) hipLaunchKernelGGL((lora_expand_kernel<TT, RS, false, true>), g, b, 0, stream, a);
@@ -298,17 +444,37 @@ hipError_t launch_expand(const LoraArgs& a, bool bf16, unsigned grid, hipStream_
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// Tokens up to which a tile's passes go to different workgroups: every token may
-// have an adapter of its own, as in decode.
+// Tokens up to which every pass of a tile has a workgroup of its own: each token may
+// have its own adapter, as in decode.
 constexpr int kSplitPassesM = 64;
 
-// Workgroups of K slices: enough to give every CU one, a wave at least four
-// 32-k steps.
+// Workgroups that share a tile's passes: one each in decode; else two, so that a
+// tile in which one request ends and the next begins takes no longer than others.
+int passes_of(int64_t M, int n, int tokens) {
+  return static_cast<int>(std::min<int64_t>({M <= kSplitPassesM ? 16 : 2, M, std::max(1, n), tokens}));
+}
+
+// Tiles of 32 tokens (each row of A read once for two fragments of tokens) where
+// there are enough of them and the ranks' rows leave LDS for it, and slices of K
+// that give every CU a workgroup, a wave at least one 64-k unit.
 void plan_shrink(LoraArgs& a, const DeviceInfo& dev) {
-  a.shrink_tiles = ceil_div(a.M, 16);
-  a.shrink_passes = a.M <= kSplitPassesM ? static_cast<int>(std::min<int64_t>({16, a.M, std::max(1, a.n)})) : 1;
-  const int want = ceil_div(std::max(1, dev.cu_count), static_cast<int64_t>(a.shrink_tiles) * a.shrink_passes);
-  a.slices = std::max(1, std::min(want, a.K / 32 / (4 * kShrinkWaves)));
+  const int cus = std::max(1, dev.cu_count);
+  a.shrink_ts = a.M > 4 * static_cast<int64_t>(cus) && a.R <= 64 ? 2 : 1;
+  a.shrink_tiles = ceil_div(a.M, 16 * a.shrink_ts);
+  a.shrink_passes = passes_of(a.M, a.n, 16 * a.shrink_ts);
+  const int64_t busy = a.M <= kSplitPassesM ? std::min<int64_t>(a.M, std::max(1, a.n)) : a.shrink_tiles;
+  a.slices = std::max(1, std::min(ceil_div(cus, busy), a.K / 64 / kShrinkWaves));
+}
+
+template <int TS>
+hipError_t launch_shrink(const LoraArgs& a, unsigned grid, hipStream_t stream) {
+  const dim3 g(grid), b(64 * kShrinkWaves);
+  if (a.R <= 16) hipLaunchKernelGGL((lora_shrink_kernel<1, TS>), g, b, 0, stream, a);
+  else if (a.R <= 32) hipLaunchKernelGGL((lora_shrink_kernel<2, TS>), g, b, 0, stream, a);
+  else if (a.R <= 64) hipLaunchKernelGGL((lora_shrink_kernel<4, TS>), g, b, 0, stream, a);
+  else if constexpr (TS == 1) hipLaunchKernelGGL((lora_shrink_kernel<8, TS>), g, b, 0, stream, a);
+  else return hipErrorInvalidValue;  // not planned
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -326,28 +492,27 @@ size_t lora_workspace_bytes(int64_t M, int K, int R, int64_t n, const DeviceInfo
 
 hipError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo& dev, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
+  const int cus = std::max(1, dev.cu_count);
   plan_shrink(a, dev);
   const int64_t shrink_grid = static_cast<int64_t>(a.shrink_tiles) * a.shrink_passes * a.slices;
   // 64 tokens a workgroup (each reads its adapters' B once for four fragments of
   // tokens) where that still gives every CU a workgroup
-  const int rounds_all = ceil_div(a.N, kChunk);
-  const int TT = static_cast<int64_t>(ceil_div(a.M, 64)) * rounds_all >= dev.cu_count && a.M > kSplitPassesM ? 4 : 1;
-  a.expand_passes = a.M <= kSplitPassesM ? static_cast<int>(std::min<int64_t>({16, a.M, std::max(1, a.n)})) : 1;
-  const int64_t tiles = ceil_div(a.M, 16 * TT);
+  const int ranges = ceil_div(a.N, kChunk);
+  const int TT = a.M > kSplitPassesM && static_cast<int64_t>(ceil_div(a.M, 64)) * ranges >= cus ? 4 : 1;
+  a.expand_tiles = ceil_div(a.M, 16 * TT);
+  a.expand_passes = passes_of(a.M, a.n, 16 * TT);
   // several ranges of n a workgroup, which share the sum over the slices, where
-  // that leaves four workgroups a CU
-  a.expand_rounds = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, tiles * rounds_all / (4 * std::max(1, dev.cu_count)))));
-  a.expand_chunks = ceil_div(rounds_all, a.expand_rounds);
-  const int64_t expand_grid = tiles * a.expand_passes * a.expand_chunks;
+  // that leaves four busy workgroups a CU
+  const int64_t busy = a.M <= kSplitPassesM ? std::min<int64_t>(a.M, std::max(1, a.n)) : a.expand_tiles;
+  a.expand_rounds = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, busy * ranges / (4 * cus))));
+  const int chunks = ceil_div(ranges, a.expand_rounds);
+  const int64_t expand_grid = static_cast<int64_t>(a.expand_tiles) * a.expand_passes * chunks;
   if (shrink_grid > 0x7FFFFFFF || expand_grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 g(static_cast<unsigned>(shrink_grid)), b(64 * kShrinkWaves);
-  if (a.n == 0) ;  // no adapter at all: only the copy below
-  else if (a.R <= 16) hipLaunchKernelGGL(lora_shrink_kernel<1>, g, b, 0, stream, a);
-  else if (a.R <= 32) hipLaunchKernelGGL(lora_shrink_kernel<2>, g, b, 0, stream, a);
-  else if (a.R <= 64) hipLaunchKernelGGL(lora_shrink_kernel<4>, g, b, 0, stream, a);
-  else hipLaunchKernelGGL(lora_shrink_kernel<8>, g, b, 0, stream, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (a.n > 0) {  // without adapters there is only the copy below
+    const unsigned sg = static_cast<unsigned>(shrink_grid);
+    const hipError_t e = a.shrink_ts == 2 ? launch_shrink<2>(a, sg, stream) : launch_shrink<1>(a, sg, stream);
+    if (e != hipSuccess) return e;
+  }
   const unsigned eg = static_cast<unsigned>(expand_grid);
   if (TT == 1)
     return a.R <= 32 ? launch_expand<1, 1>(a, bf16, eg, stream)

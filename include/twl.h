@@ -358,7 +358,7 @@ twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual
  *   workspace: twl_lora_workspace_bytes(M, K, R, n_adapters) bytes, contents on
  *              entry do not matter; calls sharing one must not run concurrently
  * K a positive multiple of 128 up to TWL_MAX_K; R a multiple of 8 from 8 to
- * TWL_LORA_MAX_R (pad A and B with zeros for other ranks); N any size; a
+ * TWL_LORA_MAX_R (pad A and B with zeros for other ranks); N at most 2^22; a
  * kind other than the two, or an output overlapping an input (other than
  * out == y), is TWL_EINVAL.  n_adapters = 0 copies y.  Values that are not finite
  * in one adapter or token reach only the tokens that use it.

@@ -137,6 +137,8 @@ twl_status twl_lora_add(const void* y, const uint16_t* x, const int32_t* ids, co
                         size_t workspace_bytes, hipStream_t stream) {
   TWL_TRY(check_lora(M, K, R, n_adapters));
   TWL_TRY(check_rows("N", N));
+  // 64 rows of fp32 y and one adapter's B stay below 2^31 bytes (32-bit offsets)
+  if (N > (int64_t{1} << 22)) return fail(TWL_ESHAPE, "N=%lld is too large", static_cast<long long>(N));
   if (kind != TWL_OUT_F32 && kind != TWL_OUT_BF16) return fail(TWL_EINVAL, "kind %d is not fp32 or bf16", kind);
   if (M == 0 || N == 0) return ok();
   TWL_REQUIRE_PTR(y);

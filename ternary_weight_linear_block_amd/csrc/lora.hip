@@ -200,6 +200,17 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
   }
 }
 
+// Loads and stores through a buffer resource: a lane whose offset is kOutside reads
+// zeros and writes nothing, so no branch stands around them (behind a branch the
+// compiler cannot count what is in flight and waits for all of it: 115 us for 4096
+// tokens of rank 64 on 17408, bf16).  Ranges stay below 2^31 bytes.
+constexpr int kRawBufferWord3 = 0x00020000;  // 32-bit data format, no swizzle: a byte count as range
+constexpr uint32_t kOutside = 0x80000000u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), kRawBufferWord3);
+}
+
 // One wave's 16 tokens x 64 n of y, in y's type, where rows are 16-byte aligned: 8
 // (fp32: 16) lanes a token, 16 bytes each.
 template <bool BF16>
@@ -212,26 +223,21 @@ struct Out {
   static __device__ __forceinline__ int token(int i, int lane) { return (64 * i + lane) / kLanes; }
   static __device__ __forceinline__ int column(int lane) { return kEach * (lane % kLanes); }
 
-  __device__ __forceinline__ void load(int i, const void* y, size_t at) {
-    raw[i] = *reinterpret_cast<const v4u*>(static_cast<const char*>(y) + at * (BF16 ? 2 : 4));
-  }
-
-  // adds d[0 ..] to item i and stores it
-  __device__ __forceinline__ void finish(int i, void* out, size_t at, const float* d) {
-    const v4u r = raw[i];
+  // adds d[0 ..] to item i
+  __device__ __forceinline__ v4u sum(int i, const float* d) const {
     v4u w;
     if constexpr (BF16) {
       const v4f lo = *reinterpret_cast<const v4f*>(d), hi = *reinterpret_cast<const v4f*>(d + 4);
       const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        w[e] = pack_bf16(__uint_as_float(r[e] << 16) + v[2 * e], __uint_as_float(r[e] & 0xFFFF0000u) + v[2 * e + 1]);
+        w[e] = pack_bf16(__uint_as_float(raw[i][e] << 16) + v[2 * e], __uint_as_float(raw[i][e] & 0xFFFF0000u) + v[2 * e + 1]);
     } else {
       const v4f v = *reinterpret_cast<const v4f*>(d);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(r[e]) + v[e]);
+      for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(raw[i][e]) + v[e]);
     }
-    *reinterpret_cast<v4u*>(static_cast<char*>(out) + at * (BF16 ? 2 : 4)) = w;
+    return w;
   }
 };
 
@@ -290,8 +296,17 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
   uint16_t* bw = b_lds[wave];
   float* dw = d_lds[wave];
   const int col = Y::column(lane);
-  const auto row = [&](int tt, int i) { return static_cast<size_t>(t0 + 16 * tt + Y::token(i, lane)) * N; };
-  const auto has = [&](uint64_t tokens, int tt, int i) { return ((tokens >> (16 * tt + Y::token(i, lane))) & 1) != 0; };
+  constexpr int kSize = BF16 ? 2 : 4;
+  const size_t tile_bytes = static_cast<size_t>(std::min<int64_t>(TM, a.M - t0)) * N * kSize;
+  const size_t tile_at = static_cast<size_t>(t0) * N * kSize;
+  const __amdgpu_buffer_rsrc_t y_buf = buffer_of(static_cast<const char*>(a.y) + tile_at, tile_bytes);
+  const __amdgpu_buffer_rsrc_t out_buf = buffer_of(static_cast<char*>(a.out) + tile_at, tile_bytes);
+  // byte offset in the tile of this lane's piece i of tokens 16 tt .. + 15 of `tokens`
+  const auto at = [&](uint64_t tokens, int tt, int i, int nb) {
+    const int t = 16 * tt + Y::token(i, lane);
+    const bool has = ((tokens >> t) & 1) != 0 && nb + col < n_hi;
+    return has ? static_cast<uint32_t>(t * N + nb + col) * kSize : kOutside;
+  };
 
   Passes passes(a.ids, t0, TM, a.M, a.n, lane);
   if (a.out != a.y && p == 0) {
@@ -303,12 +318,10 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
       for (int nb = n_lo; nb < n_hi; nb += kChunk) {
         if constexpr (VEC) {
 #pragma unroll
-          for (int i = 0; i < Y::kItems; ++i)
-            if (has(tokens, tt, i) && nb + col < N) {
-              const size_t at = (row(tt, i) + nb + col) * (BF16 ? 2 : 4);
-              *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + at) =
-                  *reinterpret_cast<const uint4*>(static_cast<const char*>(a.y) + at);
-            }
+          for (int i = 0; i < Y::kItems; ++i) {
+            const uint32_t o = at(tokens, tt, i, nb);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_amdgcn_raw_buffer_load_b128(y_buf, o, 0, 0), out_buf, o, 0, 0);
+          }
         } else {
           finish_unaligned<BF16, kOutStride>(a.y, a.out, nullptr, tokens >> (16 * tt), static_cast<size_t>(t0 + 16 * tt), N,
                                              nb, lane);
@@ -333,28 +346,26 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
   for (int skip = p; passes.next(adapter, tokens); --skip) {
     if (skip != 0) continue;
     skip = a.expand_passes;
-    const uint16_t* ba = a.b + static_cast<size_t>(adapter) * N * R;
+    const __amdgpu_buffer_rsrc_t b_buf =
+        buffer_of(a.b + static_cast<size_t>(adapter) * N * R, static_cast<size_t>(N) * R * 2);
     v4u braw[BL];
     Y y[AHEAD];
+    // pieces past the 64 rows (a rank below 32 RS) are not used, those past the
+    // adapter's end are zeros
     const auto load_b = [&](int nb) {
-      // pieces past the 64 rows (a rank below 32 RS) are not used; those past the
-      // adapter's end re-read its last one
-      const size_t first = static_cast<size_t>(nb) * R, last = static_cast<size_t>(N) * R - 8;
 #pragma unroll
       for (int l = 0; l < BL; ++l)
-        braw[l] = *reinterpret_cast<const v4u*>(ba + std::min<size_t>(first + 8 * (64 * l + lane), last));
+        braw[l] = __builtin_amdgcn_raw_buffer_load_b128(b_buf, nb < n_hi && l < pieces ? 2u * nb * R + 16u * (64 * l + lane) : kOutside, 0, 0);
     };
     const auto load_y = [&](int tt, int nb) {
 #pragma unroll
       for (int i = 0; i < Y::kItems; ++i)
-        if (has(tokens, tt, i) && nb + col < N) y[tt % AHEAD].load(i, a.y, row(tt, i) + nb + col);
+        y[tt % AHEAD].raw[i] = __builtin_amdgcn_raw_buffer_load_b128(y_buf, at(tokens, tt, i, nb), 0, 0);
     };
-    if (n_lo < n_hi) {
-      load_b(n_lo);
-      if (VEC) {
+    load_b(n_lo);
+    if (VEC) {
 #pragma unroll
-        for (int tt = 0; tt < AHEAD; ++tt) load_y(tt, n_lo);
-      }
+      for (int tt = 0; tt < AHEAD; ++tt) load_y(tt, n_lo);
     }
     const float scale = a.scale[adapter];
     __syncthreads();  // the previous pass has been read
@@ -388,8 +399,7 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
 #pragma unroll
       for (int l = 0; l < BL; ++l)
         if (l < pieces) *reinterpret_cast<v4u*>(bw + b_at[l]) = braw[l];
-      const bool more = nb + kChunk < n_hi;
-      if (more) load_b(nb + kChunk);
+      load_b(nb + kChunk);
       wave_lds_sync();
       v8bf w[4][RS];
 #pragma unroll
@@ -416,15 +426,15 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
         if constexpr (VEC) {
 #pragma unroll
           for (int i = 0; i < Y::kItems; ++i)
-            if (has(tokens, tt, i) && nb + col < N)
-              y[tt % AHEAD].finish(i, a.out, row(tt, i) + nb + col, dw + Y::token(i, lane) * kOutStride + col);
+            __builtin_amdgcn_raw_buffer_store_b128(y[tt % AHEAD].sum(i, dw + Y::token(i, lane) * kOutStride + col), out_buf,
+                                                   at(tokens, tt, i, nb), 0, 0);
+          if (tt + AHEAD < TT)
+            load_y(tt + AHEAD, nb);
+          else
+            load_y(tt + AHEAD - TT, nb + kChunk);
         } else {
           finish_unaligned<BF16, kOutStride>(a.y, a.out, dw, tokens >> (16 * tt), static_cast<size_t>(t0 + 16 * tt), N, nb,
                                              lane);
-        }
-        if constexpr (VEC) {
-          if (tt + AHEAD < TT) load_y(tt + AHEAD, nb);
-          else if (more) load_y(tt + AHEAD - TT, nb + kChunk);
         }
       }
     }

@@ -35,7 +35,6 @@ typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kShrinkWaves = 8;
 constexpr int kExpandWaves = 4;
-constexpr int kChunk = 64 * kExpandWaves;  // n of one round of an expand workgroup
 
 __device__ __forceinline__ v8bf load8(const uint16_t* p) { return *reinterpret_cast<const v8bf*>(p); }
 
@@ -263,83 +262,101 @@ __device__ __forceinline__ void finish_unaligned(const void* y, void* out, const
   }
 }
 
-// Work item (chunk, tile, p): passes p, p + passes, ... of 16 TT tokens over
-// `expand_rounds` ranges of kChunk n, 64 n a wave.  RS: 32-rank steps.
+// LDS-only workgroup barrier: this wave's LDS operations have completed, then the
+// waves meet (loads and stores in flight are not waited for).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Work item (chunk, tile, p): passes p, p + passes, ... of 16 WT tokens over an even
+// share of the ranges of 64 WN n, WN = 4 / WT.  A wave has 16 tokens x 64 n: with
+// WT = 4 the waves share B's 64 rows, with WT = 1 (few tokens) each has its own.
+// RS: 32-rank steps.
 //
 // As in the shrink kernel nothing is read or written in the matrix layout, whose
 // lanes lie a row of y apart (measured with it: 145 us for 4096 tokens of rank 64
-// on 17408, bf16): B's 64 rows are one piece of memory, copied to the wave's LDS
-// in order, and the products go through LDS to where y's 16-byte pieces are.  B and
-// y of the next range are on their way while this one is computed.
-template <int TT, int RS, bool BF16, bool VEC>
+// on 17408, bf16): B's 64 rows are one piece of memory, copied to LDS in order, and
+// the products go through LDS to where y's 16-byte pieces are.  v stays in
+// registers; the next range's B and the next two's y are on their way while one is
+// computed.
+template <int WT, int RS, bool BF16, bool VEC>
 __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs a) {
   using Y = Out<BF16>;
-  constexpr int TM = 16 * TT, TERMS = BF16 ? 2 : 3;
-  // fragments of tokens whose y is loaded ahead: 8 KB a wave in flight
-  constexpr int AHEAD = BF16 ? TT : (TT < 2 ? TT : 2);
+  constexpr int TM = 16 * WT, WN = kExpandWaves / WT, TERMS = BF16 ? 2 : 3;
   constexpr int kStride = 32 * RS + 8;  // bf16 of a row of v or B, padded
   constexpr int kOutStride = 64 + 4;    // floats of a token's products, padded
-  constexpr int BL = 4 * RS;            // 16-byte loads a lane for 64 rows of B of full rank
-  __shared__ __attribute__((aligned(16))) uint16_t vt[TERMS][TM * kStride];
-  __shared__ __attribute__((aligned(16))) uint16_t b_lds[kExpandWaves][64 * kStride];
-  __shared__ __attribute__((aligned(16))) float d_lds[kExpandWaves][16 * kOutStride];
+  constexpr int BL = 4 * RS / WT;       // 16-byte loads a lane for 64 rows of B of full rank
+  constexpr int NB = WT > 1 ? 2 : 1;    // buffers of B: shared ones alternate (one barrier a range)
+  constexpr int kSize = BF16 ? 2 : 4;
+  static_assert(BL >= 1, "loads of B");
+  __shared__ __attribute__((aligned(16))) uint16_t b_lds[NB][WN][64 * kStride];
+  // v's terms before the loop, then the products
+  constexpr int kTermBytes = TERMS * TM * kStride * 2, kOutBytes = kExpandWaves * 16 * kOutStride * 4;
+  __shared__ __attribute__((aligned(16))) char vd_lds[kTermBytes > kOutBytes ? kTermBytes : kOutBytes];
+  uint16_t* vt = reinterpret_cast<uint16_t*>(vd_lds);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wt = wave % WT, wn = wave / WT;
   const int j = lane & 15, q = lane >> 4;
   const uint32_t item = xcd_item(blockIdx.x, gridDim.x), first = item / a.expand_passes;
   const int p = item - first * a.expand_passes;
   const int chunk = first / a.expand_tiles, tile = first - chunk * a.expand_tiles;
   const int64_t t0 = static_cast<int64_t>(tile) * TM;
   const int N = a.N, R = a.R;
-  const int n_lo = chunk * a.expand_rounds * kChunk + 64 * wave;
-  const int n_hi = min(N, (chunk + 1) * a.expand_rounds * kChunk);
-  uint16_t* bw = b_lds[wave];
-  float* dw = d_lds[wave];
+  const int step = 64 * WN, ranges = (N + step - 1) / step;
+  // this wave's 64 n of the chunk's ranges: n_lo, n_lo + step, ... below n_hi
+  const int n_lo = static_cast<int>(static_cast<int64_t>(ranges) * chunk / a.expand_chunks) * step + 64 * wn;
+  const int n_hi = min(N, static_cast<int>(static_cast<int64_t>(ranges) * (chunk + 1) / a.expand_chunks) * step);
+  const int n_end = n_hi + 64 * wn;  // every wave goes round as often as the first
+  float* dw = reinterpret_cast<float*>(vd_lds) + wave * 16 * kOutStride;
   const int col = Y::column(lane);
-  constexpr int kSize = BF16 ? 2 : 4;
   const size_t tile_bytes = static_cast<size_t>(std::min<int64_t>(TM, a.M - t0)) * N * kSize;
   const size_t tile_at = static_cast<size_t>(t0) * N * kSize;
   const __amdgpu_buffer_rsrc_t y_buf = buffer_of(static_cast<const char*>(a.y) + tile_at, tile_bytes);
   const __amdgpu_buffer_rsrc_t out_buf = buffer_of(static_cast<char*>(a.out) + tile_at, tile_bytes);
-  // byte offset in the tile of this lane's piece i of tokens 16 tt .. + 15 of `tokens`
-  const auto at = [&](uint64_t tokens, int tt, int i, int nb) {
-    const int t = 16 * tt + Y::token(i, lane);
-    const bool has = ((tokens >> t) & 1) != 0 && nb + col < n_hi;
-    return has ? static_cast<uint32_t>(t * N + nb + col) * kSize : kOutside;
-  };
 
   Passes passes(a.ids, t0, TM, a.M, a.n, lane);
+  // byte offset in the tile of this lane's piece i at n = 0 for the wave's tokens of
+  // `tokens`, kOutside for others (adding n leaves it outside: rows stay below 2^30)
+  const auto piece = [&](uint64_t tokens, int i) {
+    const int t = 16 * wt + Y::token(i, lane);
+    return ((tokens >> t) & 1) != 0 ? static_cast<uint32_t>(t * N + col) * kSize : kOutside;
+  };
+  const auto at = [&](uint32_t piece0, int nb) { return nb + col < n_hi ? piece0 + static_cast<uint32_t>(nb) * kSize : kOutside; };
+  const size_t row0 = static_cast<size_t>(t0 + 16 * wt);
+
   if (a.out != a.y && p == 0) {
     // tokens without an adapter
     const uint64_t tokens = __ballot(passes.id < 0 && lane < TM && t0 + lane < a.M);
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-      if (((tokens >> (16 * tt)) & 0xFFFF) == 0) continue;
-      for (int nb = n_lo; nb < n_hi; nb += kChunk) {
+    if (((tokens >> (16 * wt)) & 0xFFFF) != 0) {
+      for (int nb = n_lo; nb < n_hi; nb += step) {
         if constexpr (VEC) {
 #pragma unroll
           for (int i = 0; i < Y::kItems; ++i) {
-            const uint32_t o = at(tokens, tt, i, nb);
+            const uint32_t o = at(piece(tokens, i), nb);
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_amdgcn_raw_buffer_load_b128(y_buf, o, 0, 0), out_buf, o, 0, 0);
           }
         } else {
-          finish_unaligned<BF16, kOutStride>(a.y, a.out, nullptr, tokens >> (16 * tt), static_cast<size_t>(t0 + 16 * tt), N,
-                                             nb, lane);
+          finish_unaligned<BF16, kOutStride>(a.y, a.out, nullptr, tokens >> (16 * wt), row0, N, nb, lane);
         }
       }
     }
   }
-  // the 16-byte pieces of 64 rows of B, R / 8 a row: piece 64 l + lane for l < R / 8
-  const int pieces = R / 8;
-  int b_at[BL];  // where it goes in bw
+  // the 16-byte pieces of 64 rows of B, R / 8 a row, by their place in memory: where
+  // this lane's go in LDS
+  const int pieces = 8 * R, first_piece = 64 * wt + lane;
+  uint32_t b_at[BL];
 #pragma unroll
   for (int l = 0; l < BL; ++l) {
-    const int c = 64 * l + lane;
-    b_at[l] = (c / pieces) * kStride + 8 * (c % pieces);
+    const uint32_t c = first_piece + 64 * WT * l, r = c / (static_cast<uint32_t>(R) / 8u);
+    b_at[l] = r * kStride + 8 * (c - r * (R / 8));
   }
-  if (pieces < BL) {  // the columns past the rank stay zero: v is zero there, B has to be finite
-    for (int e = lane; e < 64 * kStride / 8; e += 64) *reinterpret_cast<uint4*>(bw + 8 * e) = make_uint4(0, 0, 0, 0);
-    wave_lds_sync();
+  if (R < 32 * RS) {  // the columns past the rank stay zero: v is zero there, B has to be finite
+    for (uint32_t e = threadIdx.x; e < sizeof(b_lds) / 16; e += 64 * kExpandWaves)
+      reinterpret_cast<v4u*>(&b_lds[0][0][0])[e] = v4u{0, 0, 0, 0};
+    lds_barrier();
   }
   int adapter;
   uint64_t tokens;
@@ -349,26 +366,28 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
     const __amdgpu_buffer_rsrc_t b_buf =
         buffer_of(a.b + static_cast<size_t>(adapter) * N * R, static_cast<size_t>(N) * R * 2);
     v4u braw[BL];
-    Y y[AHEAD];
-    // pieces past the 64 rows (a rank below 32 RS) are not used, those past the
-    // adapter's end are zeros
-    const auto load_b = [&](int nb) {
+    const auto load_b = [&](int nb) {  // rows past the adapter's end are zeros
 #pragma unroll
-      for (int l = 0; l < BL; ++l)
-        braw[l] = __builtin_amdgcn_raw_buffer_load_b128(b_buf, nb < n_hi && l < pieces ? 2u * nb * R + 16u * (64 * l + lane) : kOutside, 0, 0);
+      for (int l = 0; l < BL; ++l) {
+        const int c = first_piece + 64 * WT * l;
+        braw[l] = __builtin_amdgcn_raw_buffer_load_b128(b_buf, nb < n_hi && c < pieces ? 2u * nb * R + 16u * c : kOutside, 0, 0);
+      }
     };
-    const auto load_y = [&](int tt, int nb) {
+    uint32_t own[Y::kItems];
 #pragma unroll
-      for (int i = 0; i < Y::kItems; ++i)
-        y[tt % AHEAD].raw[i] = __builtin_amdgcn_raw_buffer_load_b128(y_buf, at(tokens, tt, i, nb), 0, 0);
+    for (int i = 0; i < Y::kItems; ++i) own[i] = piece(tokens, i);
+    const auto load_y = [&](Y& y, int nb) {
+#pragma unroll
+      for (int i = 0; i < Y::kItems; ++i) y.raw[i] = __builtin_amdgcn_raw_buffer_load_b128(y_buf, at(own[i], nb), 0, 0);
     };
+    Y even, odd;
     load_b(n_lo);
     if (VEC) {
-#pragma unroll
-      for (int tt = 0; tt < AHEAD; ++tt) load_y(tt, n_lo);
+      load_y(even, n_lo);
+      load_y(odd, n_lo + step);
     }
     const float scale = a.scale[adapter];
-    __syncthreads();  // the previous pass has been read
+    lds_barrier();  // the previous pass's products have been read
     for (int e = threadIdx.x; e < TM * (32 * RS / 4); e += 64 * kExpandWaves) {
       const int tok = e / (32 * RS / 4), r = 4 * (e % (32 * RS / 4));
       v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -390,65 +409,65 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
         const uint2 b = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
         v -= v4f{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u), __uint_as_float(b.y << 16),
                  __uint_as_float(b.y & 0xFFFF0000u)};
-        *reinterpret_cast<uint2*>(&vt[term][tok * kStride + r]) = b;
+        *reinterpret_cast<uint2*>(vt + (term * TM + tok) * kStride + r) = b;
       }
     }
-    __syncthreads();
-    for (int nb = n_lo; nb < n_hi; nb += kChunk) {
-      wave_lds_sync();  // the previous range's B has been read
+    lds_barrier();
+    v8bf v[TERMS][RS];
+#pragma unroll
+    for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+      for (int s = 0; s < RS; ++s) v[term][s] = load8(vt + (term * TM + 16 * wt + j) * kStride + 32 * s + 8 * q);
+    lds_barrier();  // v's place takes the products
+    const auto range = [&](Y& y, int nb, int buf) {
+      uint16_t* bw = b_lds[WT > 1 ? buf : 0][wn];
+      if (WT == 1) wave_lds_sync();  // the previous range's B has been read
 #pragma unroll
       for (int l = 0; l < BL; ++l)
-        if (l < pieces) *reinterpret_cast<v4u*>(bw + b_at[l]) = braw[l];
-      load_b(nb + kChunk);
-      wave_lds_sync();
-      v8bf w[4][RS];
+        if (first_piece + 64 * WT * l < pieces) *reinterpret_cast<v4u*>(bw + b_at[l]) = braw[l];
+      load_b(nb + step);
+      if (WT == 1) wave_lds_sync();
+      else lds_barrier();
+      v4f acc[4] = {v4f{0}, v4f{0}, v4f{0}, v4f{0}};
 #pragma unroll
-      for (int f = 0; f < 4; ++f)
+      for (int s = 0; s < RS; ++s) {
+        v8bf w[4];
 #pragma unroll
-        for (int s = 0; s < RS; ++s) w[f][s] = load8(bw + (16 * f + j) * kStride + 32 * s + 8 * q);
+        for (int f = 0; f < 4; ++f) w[f] = load8(bw + (16 * f + j) * kStride + 32 * s + 8 * q);
 #pragma unroll
-      for (int tt = 0; tt < TT; ++tt) {
-        if (!VEC && ((tokens >> (16 * tt)) & 0xFFFF) == 0) continue;  // VEC: keeps the loads ahead in step
-        v4f acc[4] = {v4f{0}, v4f{0}, v4f{0}, v4f{0}};
+        for (int term = 0; term < TERMS; ++term)
 #pragma unroll
-        for (int s = 0; s < RS; ++s)
-#pragma unroll
-          for (int term = 0; term < TERMS; ++term) {
-            const v8bf v = load8(&vt[term][(16 * tt + j) * kStride + 32 * s + 8 * q]);
-#pragma unroll
-            for (int f = 0; f < 4; ++f) acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[f][s], v, acc[f], 0, 0, 0);
-          }
-        // lane (j, q) holds n = nb + 16 f + 4 q .. + 3 of token j
-        wave_lds_sync();  // the previous products have been read
-#pragma unroll
-        for (int f = 0; f < 4; ++f) *reinterpret_cast<v4f*>(dw + j * kOutStride + 16 * f + 4 * q) = acc[f];
-        wave_lds_sync();
-        if constexpr (VEC) {
-#pragma unroll
-          for (int i = 0; i < Y::kItems; ++i)
-            __builtin_amdgcn_raw_buffer_store_b128(y[tt % AHEAD].sum(i, dw + Y::token(i, lane) * kOutStride + col), out_buf,
-                                                   at(tokens, tt, i, nb), 0, 0);
-          if (tt + AHEAD < TT)
-            load_y(tt + AHEAD, nb);
-          else
-            load_y(tt + AHEAD - TT, nb + kChunk);
-        } else {
-          finish_unaligned<BF16, kOutStride>(a.y, a.out, dw, tokens >> (16 * tt), static_cast<size_t>(t0 + 16 * tt), N, nb,
-                                             lane);
-        }
+          for (int f = 0; f < 4; ++f) acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[f], v[term][s], acc[f], 0, 0, 0);
       }
+      // lane (j, q) holds n = nb + 16 f + 4 q .. + 3 of token j
+      wave_lds_sync();  // the previous products have been read
+#pragma unroll
+      for (int f = 0; f < 4; ++f) *reinterpret_cast<v4f*>(dw + j * kOutStride + 16 * f + 4 * q) = acc[f];
+      wave_lds_sync();
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < Y::kItems; ++i)
+          __builtin_amdgcn_raw_buffer_store_b128(y.sum(i, dw + Y::token(i, lane) * kOutStride + col), out_buf, at(own[i], nb), 0, 0);
+        load_y(y, nb + 2 * step);
+      } else {
+        finish_unaligned<BF16, kOutStride>(a.y, a.out, dw, tokens >> (16 * wt), row0, N, nb, lane);
+      }
+    };
+    for (int nb = n_lo; nb < n_end; nb += 2 * step) {
+      range(even, nb, 0);
+      if (nb + step < n_end) range(odd, nb + step, 1);
     }
   }
 }
 
-template <int TT, int RS>
+template <int WT, int RS>
 hipError_t launch_expand(const LoraArgs& a, bool bf16, unsigned grid, hipStream_t stream) {
   const dim3 g(grid), b(64 * kExpandWaves);
   const bool vec = a.N % (bf16 ? 8 : 4) == 0;  // rows of y 16-byte aligned
-  if (bf16 && vec) hipLaunchKernelGGL((lora_expand_kernel<TT, RS, true, true>), g, b, 0, stream, a);
-  else if (bf16) hipLaunchKernelGGL((lora_expand_kernel<TT, RS, true, false>), g, b, 0, stream, a);
-  else if (vec) hipLaunchKernelGGL((lora_expand_kernel<TT, RS, false, true>), g, b, 0, stream, a);
-  else hipLaunchKernelGGL((lora_expand_kernel<TT, RS, false, false>), g, b, 0, stream, a);
+  if (bf16 && vec) hipLaunchKernelGGL((lora_expand_kernel<WT, RS, true, true>), g, b, 0, stream, a);
+  else if (bf16) hipLaunchKernelGGL((lora_expand_kernel<WT, RS, true, false>), g, b, 0, stream, a);
+  else if (vec) hipLaunchKernelGGL((lora_expand_kernel<WT, RS, false, true>), g, b, 0, stream, a);
+  else hipLaunchKernelGGL((lora_expand_kernel<WT, RS, false, false>), g, b, 0, stream, a);
   return hipGetLastError();
 }
 
@@ -505,18 +524,15 @@ hipError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo& dev, hipStream_t
   const int cus = std::max(1, dev.cu_count);
   plan_shrink(a, dev);
   const int64_t shrink_grid = static_cast<int64_t>(a.shrink_tiles) * a.shrink_passes * a.slices;
-  // 64 tokens a workgroup (each reads its adapters' B once for four fragments of
-  // tokens) where that still gives every CU a workgroup
-  const int ranges = ceil_div(a.N, kChunk);
-  const int TT = a.M > kSplitPassesM && static_cast<int64_t>(ceil_div(a.M, 64)) * ranges >= cus ? 4 : 1;
-  a.expand_tiles = ceil_div(a.M, 16 * TT);
-  a.expand_passes = passes_of(a.M, a.n, 16 * TT);
-  // several ranges of n a workgroup, which share the sum over the slices, where
-  // that leaves four busy workgroups a CU
+  // 64 tokens a workgroup (which read B once) where that still gives every CU a
+  // workgroup, else 16 tokens and 256 n
+  const int WT = a.M > kSplitPassesM && static_cast<int64_t>(ceil_div(a.M, 64)) * ceil_div(a.N, 64) >= cus ? 4 : 1;
+  a.expand_tiles = ceil_div(a.M, 16 * WT);
+  a.expand_passes = passes_of(a.M, a.n, 16 * WT);
+  // chunks of n: one round of the workgroups that are resident at once (four a CU)
   const int64_t busy = a.M <= kSplitPassesM ? std::min<int64_t>(a.M, std::max(1, a.n)) : a.expand_tiles;
-  a.expand_rounds = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, busy * ranges / (4 * cus))));
-  const int chunks = ceil_div(ranges, a.expand_rounds);
-  const int64_t expand_grid = static_cast<int64_t>(a.expand_tiles) * a.expand_passes * chunks;
+  a.expand_chunks = static_cast<uint32_t>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.N, 256 / WT), 4 * cus / busy)));
+  const int64_t expand_grid = static_cast<int64_t>(a.expand_tiles) * a.expand_passes * a.expand_chunks;
   if (shrink_grid > 0x7FFFFFFF || expand_grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   if (a.n > 0) {  // without adapters there is only the copy below
     const unsigned sg = static_cast<unsigned>(shrink_grid);
@@ -524,7 +540,7 @@ hipError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo& dev, hipStream_t
     if (e != hipSuccess) return e;
   }
   const unsigned eg = static_cast<unsigned>(expand_grid);
-  if (TT == 1)
+  if (WT == 1)
     return a.R <= 32 ? launch_expand<1, 1>(a, bf16, eg, stream)
            : a.R <= 64 ? launch_expand<1, 2>(a, bf16, eg, stream) : launch_expand<1, 4>(a, bf16, eg, stream);
   return a.R <= 32 ? launch_expand<4, 1>(a, bf16, eg, stream)

@@ -154,8 +154,7 @@ struct LoraArgs {
   int N, K, R, n;
   int slices, shrink_ts;
   uint32_t shrink_tiles, shrink_passes;
-  int expand_rounds;
-  uint32_t expand_tiles, expand_passes;
+  uint32_t expand_chunks, expand_tiles, expand_passes;
 };
 size_t lora_workspace_bytes(int64_t M, int K, int R, int64_t n, const DeviceInfo& dev);
 hipError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo& dev, hipStream_t stream);

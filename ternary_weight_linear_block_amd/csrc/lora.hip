@@ -33,7 +33,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
-constexpr int kShrinkWaves = 8;
+constexpr int shrink_waves(int ts) { return ts == 1 ? 8 : 4; }  // with 32 tokens, LDS for three workgroups a CU
 constexpr int kExpandWaves = 4;
 
 __device__ __forceinline__ v8bf load8(const uint16_t* p) { return *reinterpret_cast<const v8bf*>(p); }
@@ -97,7 +97,8 @@ __device__ __forceinline__ void wave_lds_sync() {
 // (16-byte units swizzled by row, no bank conflicts): no barrier before the sums
 // meet.
 template <int RT, int TS>
-__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs a) {
+__global__ __launch_bounds__(64 * shrink_waves(TS)) void lora_shrink_kernel(LoraArgs a) {
+  constexpr int kShrinkWaves = shrink_waves(TS);
   constexpr int TM = 16 * TS;
   constexpr int kStride = 16 * RT + 4;  // floats of a token's row of sums, padded
   constexpr int G = 2 * (TS + RT);      // groups of 8 rows: x, then A
@@ -133,6 +134,15 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
     return *reinterpret_cast<const v8bf*>(stage + at);
   };
 
+  v4u raw[U][G];
+  const auto load = [&](int g0, int g1, const char* base, int u) {  // units past the last re-read it and are not multiplied
+#pragma unroll
+    for (int v = 0; v < U; ++v)
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (g >= g0 && g < g1) raw[v][g] = *reinterpret_cast<const v4u*>(base + off[g] + 128 * max(min(u + v, u1 - 1), 0));
+  };
+  constexpr int kAll = 2 * TS;  // groups of x
   Passes passes(a.ids, t0, TM, a.M, a.n, lane);
   int adapter;
   uint64_t tokens;
@@ -145,22 +155,16 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
     for (int h = 0; h < TS; ++h)
 #pragma unroll
       for (int f = 0; f < RT; ++f) acc[h][f] = v4f{0};
-    v4u raw[U][G];
-    const auto load = [&](int u) {  // units past the last re-read it and are not multiplied
-#pragma unroll
-      for (int v = 0; v < U; ++v)
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-          raw[v][g] = *reinterpret_cast<const v4u*>((g < 2 * TS ? xb : ab) + off[g] + 128 * min(u + v, u1 - 1));
-    };
-    if (u0 < u1) load(u0);
+    load(0, kAll, xb, u0);
+    load(kAll, G, ab, u0);
     for (int u = u0; u < u1; u += U) {
       wave_lds_sync();  // the previous units have been read
 #pragma unroll
       for (int v = 0; v < U; ++v)
 #pragma unroll
         for (int g = 0; g < G; ++g) *reinterpret_cast<v4u*>(stage + (v * G + g) * 1024 + put) = raw[v][g];
-      if (u + U < u1) load(u + U);
+      load(0, kAll, xb, u + U);
+      load(kAll, G, ab, u + U);
       wave_lds_sync();
 #pragma unroll
       for (int v = 0; v < U; ++v) {
@@ -252,7 +256,7 @@ __device__ __forceinline__ void finish_unaligned(const void* y, void* out, const
   for (int t = 0; t < 16; ++t) {
     if (((tokens >> t) & 1) == 0) continue;
     const size_t at = at0 + static_cast<size_t>(t) * N;
-    const float add = d != nullptr ? d[t * kStride + lane] : 0.0f;
+    const float add = d != nullptr ? d[t * kStride + lane] : -0.0f;
     if constexpr (BF16) {
       const float v = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(y)[at]) << 16);
       static_cast<uint16_t*>(out)[at] = static_cast<uint16_t>(pack_bf16(v + add, 0.0f));
@@ -327,22 +331,28 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
   const auto at = [&](uint32_t piece0, int nb) { return nb + col < n_hi ? piece0 + static_cast<uint32_t>(nb) * kSize : kOutside; };
   const size_t row0 = static_cast<size_t>(t0 + 16 * wt);
 
-  if (a.out != a.y && p == 0) {
-    // tokens without an adapter
-    const uint64_t tokens = __ballot(passes.id < 0 && lane < TM && t0 + lane < a.M);
-    if (((tokens >> (16 * wt)) & 0xFFFF) != 0) {
-      for (int nb = n_lo; nb < n_hi; nb += step) {
-        if constexpr (VEC) {
+  // tokens without an adapter: copied with the tile's first pass, or here if it has none
+  uint64_t none = a.out != a.y && p == 0 ? __ballot(passes.id < 0 && lane < TM && t0 + lane < a.M) : 0;
+  if (passes.rest == 0) {
+    for (int nb = n_lo; nb < n_hi; nb += 4 * step) {
+      if constexpr (VEC) {
+        v4u y[4][Y::kItems];
 #pragma unroll
-          for (int i = 0; i < Y::kItems; ++i) {
-            const uint32_t o = at(piece(tokens, i), nb);
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_amdgcn_raw_buffer_load_b128(y_buf, o, 0, 0), out_buf, o, 0, 0);
-          }
-        } else {
-          finish_unaligned<BF16, kOutStride>(a.y, a.out, nullptr, tokens >> (16 * wt), row0, N, nb, lane);
-        }
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < Y::kItems; ++i)
+            y[u][i] = __builtin_amdgcn_raw_buffer_load_b128(y_buf, at(piece(none, i), nb + u * step), 0, 0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < Y::kItems; ++i)
+            __builtin_amdgcn_raw_buffer_store_b128(y[u][i], out_buf, at(piece(none, i), nb + u * step), 0, 0);
+      } else {
+        for (int u = 0; u < 4 && nb + u * step < n_hi; ++u)
+          finish_unaligned<BF16, kOutStride>(a.y, a.out, nullptr, none >> (16 * wt), row0, N, nb + u * step, lane);
       }
     }
+    return;
   }
   // the 16-byte pieces of 64 rows of B, R / 8 a row, by their place in memory: where
   // this lane's go in LDS
@@ -373,9 +383,12 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
         braw[l] = __builtin_amdgcn_raw_buffer_load_b128(b_buf, nb < n_hi && c < pieces ? 2u * nb * R + 16u * c : kOutside, 0, 0);
       }
     };
+    const uint64_t written = tokens | none;
+    const bool copied = ((none >> (16 * wt + j)) & 1) != 0;  // token j takes nothing from this adapter
+    none = 0;
     uint32_t own[Y::kItems];
 #pragma unroll
-    for (int i = 0; i < Y::kItems; ++i) own[i] = piece(tokens, i);
+    for (int i = 0; i < Y::kItems; ++i) own[i] = piece(written, i);
     const auto load_y = [&](Y& y, int nb) {
 #pragma unroll
       for (int i = 0; i < Y::kItems; ++i) y.raw[i] = __builtin_amdgcn_raw_buffer_load_b128(y_buf, at(own[i], nb), 0, 0);
@@ -388,8 +401,8 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
     }
     const float scale = a.scale[adapter];
     lds_barrier();  // the previous pass's products have been read
-    for (int e = threadIdx.x; e < TM * (32 * RS / 4); e += 64 * kExpandWaves) {
-      const int tok = e / (32 * RS / 4), r = 4 * (e % (32 * RS / 4));
+    for (int e = threadIdx.x; e < TM * 8 * RS; e += 64 * kExpandWaves) {
+      const int tok = e / (8 * RS), r = 4 * (e % (8 * RS));
       v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
       if (r < R && ((tokens >> tok) & 1)) {
         const float* src = a.part + static_cast<size_t>(t0 + tok) * R + r;
@@ -442,7 +455,10 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
       // lane (j, q) holds n = nb + 16 f + 4 q .. + 3 of token j
       wave_lds_sync();  // the previous products have been read
 #pragma unroll
-      for (int f = 0; f < 4; ++f) *reinterpret_cast<v4f*>(dw + j * kOutStride + 16 * f + 4 * q) = acc[f];
+      for (int f = 0; f < 4; ++f) {
+        if (copied) acc[f] = v4f{-0.0f, -0.0f, -0.0f, -0.0f};  // y + -0 is y
+        *reinterpret_cast<v4f*>(dw + j * kOutStride + 16 * f + 4 * q) = acc[f];
+      }
       wave_lds_sync();
       if constexpr (VEC) {
 #pragma unroll
@@ -450,7 +466,7 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
           __builtin_amdgcn_raw_buffer_store_b128(y.sum(i, dw + Y::token(i, lane) * kOutStride + col), out_buf, at(own[i], nb), 0, 0);
         load_y(y, nb + 2 * step);
       } else {
-        finish_unaligned<BF16, kOutStride>(a.y, a.out, dw, tokens >> (16 * wt), row0, N, nb, lane);
+        finish_unaligned<BF16, kOutStride>(a.y, a.out, dw, written >> (16 * wt), row0, N, nb, lane);
       }
     };
     for (int nb = n_lo; nb < n_end; nb += 2 * step) {
@@ -492,12 +508,13 @@ void plan_shrink(LoraArgs& a, const DeviceInfo& dev) {
   a.shrink_tiles = ceil_div(a.M, 16 * a.shrink_ts);
   a.shrink_passes = passes_of(a.M, a.n, 16 * a.shrink_ts);
   const int64_t busy = a.M <= kSplitPassesM ? std::min<int64_t>(a.M, std::max(1, a.n)) : a.shrink_tiles;
-  a.slices = std::max(1, std::min(ceil_div(cus, busy), a.K / 64 / kShrinkWaves));
+  const int64_t want = a.shrink_ts == 1 ? cus : 2 * cus;
+  a.slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((want + busy - 1) / busy, a.K / 64 / shrink_waves(a.shrink_ts))));
 }
 
 template <int TS>
 hipError_t launch_shrink(const LoraArgs& a, unsigned grid, hipStream_t stream) {
-  const dim3 g(grid), b(64 * kShrinkWaves);
+  const dim3 g(grid), b(64 * shrink_waves(TS));
   if (a.R <= 16) hipLaunchKernelGGL((lora_shrink_kernel<1, TS>), g, b, 0, stream, a);
   else if (a.R <= 32) hipLaunchKernelGGL((lora_shrink_kernel<2, TS>), g, b, 0, stream, a);
   else if (a.R <= 64) hipLaunchKernelGGL((lora_shrink_kernel<4, TS>), g, b, 0, stream, a);
@@ -529,9 +546,16 @@ hipError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo& dev, hipStream_t
   const int WT = a.M > kSplitPassesM && static_cast<int64_t>(ceil_div(a.M, 64)) * ceil_div(a.N, 64) >= cus ? 4 : 1;
   a.expand_tiles = ceil_div(a.M, 16 * WT);
   a.expand_passes = passes_of(a.M, a.n, 16 * WT);
-  // chunks of n: one round of the workgroups that are resident at once (four a CU)
-  const int64_t busy = a.M <= kSplitPassesM ? std::min<int64_t>(a.M, std::max(1, a.n)) : a.expand_tiles;
-  a.expand_chunks = static_cast<uint32_t>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.N, 256 / WT), 4 * cus / busy)));
+  // ranges of n a workgroup: about one round of the workgroups that are resident at
+  // once (four a CU, idle passes of a decode batch included); and, for the sum over
+  // the slices not to outweigh y, as many as make y's bytes those of the slices
+  // while every CU has a workgroup
+  const int64_t ranges = ceil_div(a.N, 256 / WT);
+  const int64_t groups = static_cast<int64_t>(a.expand_tiles) * (a.M <= kSplitPassesM ? a.expand_passes : 1);
+  const int64_t limit = std::max<int64_t>(1, 4 * cus / groups);
+  const int64_t y_bytes = 2 * (256 / WT) * (bf16 ? 2 : 4), slice_bytes = static_cast<int64_t>(a.slices) * a.R * 4;
+  const int64_t each = std::max((ranges + limit / 2) / limit, std::min(slice_bytes / y_bytes, ranges * groups / cus));
+  a.expand_chunks = static_cast<uint32_t>(ceil_div(ranges, static_cast<int>(std::max<int64_t>(1, each))));
   const int64_t expand_grid = static_cast<int64_t>(a.expand_tiles) * a.expand_passes * a.expand_chunks;
   if (shrink_grid > 0x7FFFFFFF || expand_grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   if (a.n > 0) {  // without adapters there is only the copy below

@@ -22,7 +22,7 @@ class _Env:
         self.fp16 = (torch.float16, torch.int16)
         self.fp32, self.int32, self.int8, self.uint8 = (torch.float32,), (torch.int32,), (torch.int8,), (torch.uint8,)
         self.kinds = {torch.float32: _lib.OUT_F32, torch.bfloat16: _lib.OUT_BF16}
-        self.device = torch.cuda.current_device
+        self.device, self.empty_like = torch.cuda.current_device, torch.empty_like
         # workspace sizes by (device, sizes): the planners behind them cost 1 us a call
         self.lora_need = functools.lru_cache(4096)(lambda device, *sizes: self.lib.twl_lora_workspace_bytes(*sizes))
         self.gated_need = functools.lru_cache(4096)(lambda device, *sizes: self.lib.twl_gated_workspace_bytes(*sizes))
@@ -80,11 +80,12 @@ def _handle(stream, env, device):
 
 
 def _empty(env, like, shape, dtype, stream):
-    """A new tensor beside `like` that belongs to the stream of the call."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    with env.torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+    """A new tensor beside `like`, of its own shape unless given, that belongs to
+    the stream of the call."""
+    if stream is not None:
+        with env.torch.cuda.stream(stream):
+            return _empty(env, like, shape, dtype, None)
+    return env.empty_like(like, dtype=dtype) if shape is None else like.new_empty(shape, dtype=dtype)
 
 
 def _workspace(env, like, need, workspace, stream, device):
@@ -130,12 +131,12 @@ def norm_rotate_quant_act(x, weight, sign, eps=1e-6, residual=None, post_weight=
     if sign is not None:
         p_sign = _check(sign, "sign", row, env.int8, device)
         if x_i8 is None:
-            x_i8 = _empty(env, x, wide, env.torch.int8, stream)
+            x_i8 = _empty(env, x, None, env.int8[0], stream)
             p_x_i8 = x_i8.data_ptr()
         else:
             p_x_i8 = _check(x_i8, "x_i8", wide, env.int8, device)
         if a_scale is None:
-            a_scale = _empty(env, x, (M,), env.torch.float32, stream)
+            a_scale = _empty(env, x, (M,), env.fp32[0], stream)
             p_a_scale = a_scale.data_ptr()
         else:
             p_a_scale = _check(a_scale, "a_scale", (M,), env.fp32, device)
@@ -143,7 +144,7 @@ def norm_rotate_quant_act(x, weight, sign, eps=1e-6, residual=None, post_weight=
         raise ValueError("x_i8 and a_scale need sign")
     if residual is not None or post_weight is not None or gate is not None or branch_scale != 1.0:
         if h is None:
-            h = _empty(env, x, wide, x.dtype, stream)
+            h = _empty(env, x, None, x.dtype, stream)
             p_h = h.data_ptr()
         else:
             p_h = _check(h, "h", wide, bf16, device)
@@ -152,7 +153,7 @@ def norm_rotate_quant_act(x, weight, sign, eps=1e-6, residual=None, post_weight=
     if normed is not None:
         p_normed = _check(normed, "normed", wide, bf16, device)
     elif return_normed:
-        normed = _empty(env, x, wide, x.dtype, stream)
+        normed = _empty(env, x, None, x.dtype, stream)
         p_normed = normed.data_ptr()
     st = env.lib.twl_norm_rotate_quant_act(
         p_x, p_residual, p_post, p_gate, gate_stride, branch_scale, p_weight, eps, p_sign, M, K, p_h, p_normed,
@@ -197,7 +198,7 @@ def lora_add(y, x, ids, lora_a, lora_b, scale, out=None, workspace=None, stream=
     p_b = _check(lora_b, "lora_b", (n, N, R), env.bf16, device)
     p_scale = _check(scale, "scale", (n,), env.fp32, device)
     if out is None:
-        out = _empty(env, y, (M, N), y.dtype, stream)
+        out = _empty(env, y, None, y.dtype, stream)
         p_out = out.data_ptr()
     else:
         p_out = _check(out, "out", (M, N), like_y, device)

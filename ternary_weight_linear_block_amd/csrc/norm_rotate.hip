@@ -24,6 +24,7 @@
 #include "rotate_block.h"
 
 #include <algorithm>
+#include <atomic>
 
 namespace twl {
 namespace {
@@ -376,10 +377,15 @@ hipError_t launch_form(const NormArgs& a, const DeviceInfo& dev, hipStream_t str
   }
   // as many workgroups as are resident at once, so that all of them take the same
   // number of tokens, one more at most
-  int per_cu = 1;
-  const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(
-      &per_cu, norm_rotate_kernel<BPW, ROT, BRANCH, AHEAD, MAXT, WAVES>, 64 * nw, lds);
-  if (e != hipSuccess) return e;
+  // (asked once for each number of waves: the query costs as much as a launch)
+  static std::atomic<int> resident_of[kMaxNormWaves + 1];
+  int per_cu = resident_of[nw].load(std::memory_order_relaxed);
+  if (per_cu == 0) {
+    const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(
+        &per_cu, norm_rotate_kernel<BPW, ROT, BRANCH, AHEAD, MAXT, WAVES>, 64 * nw, lds);
+    if (e != hipSuccess) return e;
+    resident_of[nw].store(std::max(1, per_cu), std::memory_order_relaxed);
+  }
   const int64_t resident = static_cast<int64_t>(std::max(1, dev.cu_count)) * std::max(1, per_cu);
   hipLaunchKernelGGL((norm_rotate_kernel<BPW, ROT, BRANCH, AHEAD, MAXT, WAVES>), dim3(static_cast<unsigned>(std::min(a.M, resident))),
                      dim3(64 * nw), lds, stream, a);

@@ -324,7 +324,7 @@ int twl_rotate_quant_linear_fused(int64_t M, int64_t N, int64_t K);
  *   residual    in : bf16 [M, K], or NULL
  *   post_weight in : bf16 [K], or NULL
  *   gate        in : bf16, row t at gate + t * gate_stride elements (0: one row
- *                    [K] for all tokens; else a multiple of 8, at least K), or NULL
+ *                    [K] for all tokens; else a multiple of 8 from K to 2^30), or NULL
  *   weight      in : bf16 [K];  sign in: int8 +-1 [K], or NULL: no rotation
  *   h           out: bf16 [M, K], or NULL; may be x or residual themselves
  *   normed      out: n as bf16 [M, K], or NULL (required when sign is NULL)

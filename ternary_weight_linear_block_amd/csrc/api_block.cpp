@@ -191,8 +191,8 @@ twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual
   TWL_TRY(check_k(K));
   if (!(eps > 0.0) || !std::isfinite(eps)) return fail(TWL_EINVAL, "eps=%g must be positive and finite", eps);
   if (!std::isfinite(branch_scale)) return fail(TWL_EINVAL, "branch_scale=%g must be finite", branch_scale);
-  if (gate_stride != 0 && (gate_stride < K || gate_stride % 8 != 0 || gate_stride > (int64_t{1} << 40)))
-    return fail(TWL_ESHAPE, "gate_stride=%lld must be 0 or a multiple of 8 of at least K=%lld",
+  if (gate_stride != 0 && (gate_stride < K || gate_stride % 8 != 0 || gate_stride > (int64_t{1} << 30)))
+    return fail(TWL_ESHAPE, "gate_stride=%lld must be 0 or a multiple of 8 from K=%lld to 2^30",
                 static_cast<long long>(gate_stride), static_cast<long long>(K));
   const bool branch = residual != nullptr || post_weight != nullptr || gate != nullptr || branch_scale != 1.0;
   if (h != nullptr && !branch)

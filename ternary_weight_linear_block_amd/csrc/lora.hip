@@ -60,7 +60,7 @@ struct Passes {
   }
 };
 
-// Workgroups are dispatched to the XCDs in turn: work item of workgroup `bid` such
+// Workgroups are dispatched to the XCDs in turn: work item of workgroup `bid` of `total` such
 // that each XCD gets a contiguous range of the items, whose neighbours share an
 // adapter's rows in its L2.
 __device__ __forceinline__ int xcd_item(int bid, int total) {
@@ -108,9 +108,10 @@ __global__ __launch_bounds__(64 * shrink_waves(TS)) void lora_shrink_kernel(Lora
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j = lane & 15, q = lane >> 4;
-  const uint32_t item = xcd_item(blockIdx.x, gridDim.x), first = item / a.shrink_passes;
-  const int p = item - first * a.shrink_passes;
-  const int slice = first / a.shrink_tiles, tile = first - slice * a.shrink_tiles;
+  const uint32_t items = a.slices * a.shrink_tiles;
+  const int p = blockIdx.x / items;
+  const uint32_t item = xcd_item(blockIdx.x - p * items, items);
+  const int slice = item / a.shrink_tiles, tile = item - slice * a.shrink_tiles;
   const int64_t t0 = static_cast<int64_t>(tile) * TM;
   const int K = a.K, R = a.R;
   // this wave's 64-k units
@@ -304,9 +305,10 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wt = wave % WT, wn = wave / WT;
   const int j = lane & 15, q = lane >> 4;
-  const uint32_t item = xcd_item(blockIdx.x, gridDim.x), first = item / a.expand_passes;
-  const int p = item - first * a.expand_passes;
-  const int chunk = first / a.expand_tiles, tile = first - chunk * a.expand_tiles;
+  const uint32_t items = a.expand_chunks * a.expand_tiles;
+  const int p = blockIdx.x / items;
+  const uint32_t item = xcd_item(blockIdx.x - p * items, items);
+  const int chunk = item / a.expand_tiles, tile = item - chunk * a.expand_tiles;
   const int64_t t0 = static_cast<int64_t>(tile) * TM;
   const int N = a.N, R = a.R;
   const int step = 64 * WN, ranges = (N + step - 1) / step;

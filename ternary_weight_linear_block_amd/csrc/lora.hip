@@ -35,6 +35,7 @@ typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
 constexpr int shrink_waves(int ts) { return ts == 1 ? 8 : 4; }  // with 32 tokens, LDS for three workgroups a CU
 constexpr int kExpandWaves = 4;
+constexpr int kLdsBytes = 160 * 1024;  // of a CU
 
 __device__ __forceinline__ v8bf load8(const uint16_t* p) { return *reinterpret_cast<const v8bf*>(p); }
 
@@ -286,20 +287,29 @@ __device__ __forceinline__ void lds_barrier() {
 // the products go through LDS to where y's 16-byte pieces are.  v stays in
 // registers; the next range's B and the next two's y are on their way while one is
 // computed.
+constexpr int kOutStride = 64 + 4;  // floats of a token's products in LDS, padded
+
+struct ExpandLds {
+  int row;    // bf16 of a row of v or B, padded
+  int bufs;   // buffers of B: shared ones alternate (one barrier a range)
+  int b, vd;  // bytes: B; v's terms before the loop, then the products
+  constexpr ExpandLds(int wt, int rs, bool bf16)
+      : row(32 * rs + 8), bufs(wt > 1 ? 2 : 1), b(bufs * (kExpandWaves / wt) * 64 * row * 2),
+        vd(std::max((bf16 ? 2 : 3) * 16 * wt * row * 2, kExpandWaves * 16 * kOutStride * 4)) {}
+};
+
 template <int WT, int RS, bool BF16, bool VEC>
 __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs a) {
   using Y = Out<BF16>;
+  constexpr ExpandLds L(WT, RS, BF16);
   constexpr int TM = 16 * WT, WN = kExpandWaves / WT, TERMS = BF16 ? 2 : 3;
-  constexpr int kStride = 32 * RS + 8;  // bf16 of a row of v or B, padded
-  constexpr int kOutStride = 64 + 4;    // floats of a token's products, padded
-  constexpr int BL = 4 * RS / WT;       // 16-byte loads a lane for 64 rows of B of full rank
-  constexpr int NB = WT > 1 ? 2 : 1;    // buffers of B: shared ones alternate (one barrier a range)
+  constexpr int kStride = L.row, NB = L.bufs;
+  constexpr int BL = 4 * RS / WT;  // 16-byte loads a lane for 64 rows of B of full rank
   constexpr int kSize = BF16 ? 2 : 4;
   static_assert(BL >= 1, "loads of B");
   __shared__ __attribute__((aligned(16))) uint16_t b_lds[NB][WN][64 * kStride];
-  // v's terms before the loop, then the products
-  constexpr int kTermBytes = TERMS * TM * kStride * 2, kOutBytes = kExpandWaves * 16 * kOutStride * 4;
-  __shared__ __attribute__((aligned(16))) char vd_lds[kTermBytes > kOutBytes ? kTermBytes : kOutBytes];
+  static_assert(sizeof(b_lds) == L.b, "what the launcher counts");
+  __shared__ __attribute__((aligned(16))) char vd_lds[L.vd];
   uint16_t* vt = reinterpret_cast<uint16_t*>(vd_lds);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -491,14 +501,19 @@ hipError_t launch_expand(const LoraArgs& a, bool bf16, unsigned grid, hipStream_
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// Tokens up to which every pass of a tile has a workgroup of its own: each token may
-// have its own adapter, as in decode.
-constexpr int kSplitPassesM = 64;
+// Tokens up to which every pass of a tile of 16 has a workgroup of its own: each
+// token may have its own adapter.  200 tokens of 32 adapters in any order, rank 16,
+// 5120 -> 5120: 22 us, and 42 with four workgroups a tile of 64; the same as four
+// requests of rank 64: 13.5 and 16 us.
+constexpr int kSplitPassesM = 256;
 
-// Workgroups that share a tile's passes: one each in decode; else two, so that a
-// tile in which one request ends and the next begins takes no longer than others.
+// Workgroups that share a tile's passes (pass p, p + passes, ...).  Larger batches
+// have few adapters a tile, and a workgroup without a pass costs its launch: 4096
+// tokens of 24 requests take 109 us with four, 127 with one (a tile in which one
+// request ends and the next begins takes twice as long) and 117 with 16; 1500
+// tokens of 16 adapters in any order 119, and 136 with two.
 int passes_of(int64_t M, int n, int tokens) {
-  return static_cast<int>(std::min<int64_t>({M <= kSplitPassesM ? 16 : 2, M, std::max(1, n), tokens}));
+  return static_cast<int>(std::min<int64_t>({M <= kSplitPassesM ? 16 : 4, M, std::max(1, n), tokens}));
 }
 
 // Tiles of 32 tokens (each row of A read once for two fragments of tokens) where
@@ -543,20 +558,31 @@ hipError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo& dev, hipStream_t
   const int cus = std::max(1, dev.cu_count);
   plan_shrink(a, dev);
   const int64_t shrink_grid = static_cast<int64_t>(a.shrink_tiles) * a.shrink_passes * a.slices;
-  // 64 tokens a workgroup (which read B once) where that still gives every CU a
-  // workgroup, else 16 tokens and 256 n
-  const int WT = a.M > kSplitPassesM && static_cast<int64_t>(ceil_div(a.M, 64)) * ceil_div(a.N, 64) >= cus ? 4 : 1;
+  // 64 tokens a workgroup read B once, 16 tokens and 256 n make more workgroups of
+  // smaller tiles: the first where B is large against y or the grid is many times
+  // the card (4096 tokens of rank 64 on 17408: 109 against 134 us; 500 of rank 64 on
+  // 5120: 27.4 and 29.9), else the second (2048 tokens of rank 32 on 5120: 22.7
+  // against 20.9 us, 1000 of rank 16: 19.0 and 17.7)
+  const bool large = a.R > 32 || static_cast<int64_t>(ceil_div(a.M, 64)) * ceil_div(a.N, 64) >= 16 * cus;
+  const int WT = a.M > kSplitPassesM && large ? 4 : 1;
+  const int RS = a.R <= 32 ? 1 : a.R <= 64 ? 2 : 4;
   a.expand_tiles = ceil_div(a.M, 16 * WT);
   a.expand_passes = passes_of(a.M, a.n, 16 * WT);
-  // ranges of n a workgroup: about one round of the workgroups that are resident at
-  // once (four a CU, idle passes of a decode batch included); and, for the sum over
-  // the slices not to outweigh y, as many as make y's bytes those of the slices
-  // while every CU has a workgroup
+  // Ranges of n a workgroup.  Each workgroup sums the slices of its tokens and waits
+  // for its first operands, so few long ones are better, as long as they fill the
+  // card: first passes take half of the workgroups that can be resident (the other
+  // half is for the passes behind them; all of them: 4096 tokens of rank 128 on 5120
+  // 96 against 89 us, 2048 of rank 32 24 against 21; a quarter: 108 and 22).
+  // And where the slices' bytes outweigh y's, as many as level them while two of
+  // three CUs have a workgroup (500 tokens, K = 17408, N = 5120: 25 us, 27.6 with
+  // one for every CU).
+  const ExpandLds lds(WT, RS, bf16);
+  const int64_t resident = static_cast<int64_t>(std::min(4, kLdsBytes / (lds.b + lds.vd))) * cus;
   const int64_t ranges = ceil_div(a.N, 256 / WT);
   const int64_t groups = static_cast<int64_t>(a.expand_tiles) * (a.M <= kSplitPassesM ? a.expand_passes : 1);
-  const int64_t limit = std::max<int64_t>(1, 4 * cus / groups);
+  const int64_t limit = std::max<int64_t>(1, resident / 2 / groups);
   const int64_t y_bytes = 2 * (256 / WT) * (bf16 ? 2 : 4), slice_bytes = static_cast<int64_t>(a.slices) * a.R * 4;
-  const int64_t each = std::max((ranges + limit / 2) / limit, std::min(slice_bytes / y_bytes, ranges * groups / cus));
+  const int64_t each = std::max((ranges + limit / 2) / limit, std::min(slice_bytes / y_bytes, ranges * groups * 3 / (2 * cus)));
   a.expand_chunks = static_cast<uint32_t>(ceil_div(ranges, static_cast<int>(std::max<int64_t>(1, each))));
   const int64_t expand_grid = static_cast<int64_t>(a.expand_tiles) * a.expand_passes * a.expand_chunks;
   if (shrink_grid > 0x7FFFFFFF || expand_grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
@@ -567,10 +593,10 @@ hipError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo& dev, hipStream_t
   }
   const unsigned eg = static_cast<unsigned>(expand_grid);
   if (WT == 1)
-    return a.R <= 32 ? launch_expand<1, 1>(a, bf16, eg, stream)
-           : a.R <= 64 ? launch_expand<1, 2>(a, bf16, eg, stream) : launch_expand<1, 4>(a, bf16, eg, stream);
-  return a.R <= 32 ? launch_expand<4, 1>(a, bf16, eg, stream)
-         : a.R <= 64 ? launch_expand<4, 2>(a, bf16, eg, stream) : launch_expand<4, 4>(a, bf16, eg, stream);
+    return RS == 1 ? launch_expand<1, 1>(a, bf16, eg, stream)
+           : RS == 2 ? launch_expand<1, 2>(a, bf16, eg, stream) : launch_expand<1, 4>(a, bf16, eg, stream);
+  return RS == 1 ? launch_expand<4, 1>(a, bf16, eg, stream)
+         : RS == 2 ? launch_expand<4, 2>(a, bf16, eg, stream) : launch_expand<4, 4>(a, bf16, eg, stream);
 }
 
 }  // namespace twl

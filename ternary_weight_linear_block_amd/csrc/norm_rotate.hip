@@ -170,7 +170,9 @@ struct Tables {
 // ROT: rotate and quantise; else only h and n are written.  BRANCH: any of
 // post_weight, gate, branch_scale and residual is there.
 // AHEAD (one block a wave): the next token's rows are loaded while this one is
-// computed.  WAVES: waves a SIMD that the registers have to leave room for.
+// computed, from where its own operands have been used (loaded at its start they
+// cost 16 registers more: 4096 tokens of 9216 106 instead of 103 us; not ahead 114).
+// WAVES: waves a SIMD that the registers have to leave room for.
 template <int BPW, bool ROT, bool BRANCH, bool AHEAD, int MAXT, int WAVES>
 __global__ __launch_bounds__(MAXT) __attribute__((amdgpu_waves_per_eu(WAVES)))
 void norm_rotate_kernel(NormArgs a) {
@@ -220,9 +222,6 @@ void norm_rotate_kernel(NormArgs a) {
       in[0] = next;
       tab[0] = Tables{};
       load_branch_tables(0, tab[0]);
-      const int64_t tn = std::min<int64_t>(t + gridDim.x, a.M - 1);
-      load_x(tn, 0, next);
-      load_branch(tn, 0, next);
     } else {
 #pragma unroll
       for (int i = 0; i < BPW; ++i) {
@@ -292,6 +291,11 @@ void norm_rotate_kernel(NormArgs a) {
     if (BPW <= 2) {
 #pragma unroll
       for (int i = 0; i < BPW; ++i) load_tables(i, tab[i]);
+    }
+    if (AHEAD) {
+      const int64_t tn = std::min<int64_t>(t + gridDim.x, a.M - 1);
+      load_x(tn, 0, next);
+      load_branch(tn, 0, next);
     }
     double s = 0.0;
 #pragma unroll
@@ -395,7 +399,18 @@ hipError_t launch_form(const NormArgs& a, const DeviceInfo& dev, hipStream_t str
 template <bool ROT, bool BRANCH>
 hipError_t launch_blocks(const NormArgs& a, const DeviceInfo& dev, hipStream_t stream) {
   const int nblocks = a.K / kBlock;  // 1 .. 64 (validated by the caller)
-  if (nblocks <= 8) return launch_form<1, ROT, BRANCH, true, 512, 4>(a, dev, stream);
+  // One block a wave up to 16, the next token's rows ahead: a token's latency is
+  // lowest (5120: 5.8 us, two blocks a wave 6.7), and many tokens keep the memory
+  // busiest (each call followed by one that reads x_i8, both: 8192 tokens of 5120
+  // with everything 216 us, two blocks a wave without rows ahead 232, with them and
+  // half the waves 226; 4096 of 12288 256 against 291).  The exception is the norm alone,
+  // whose few operands leave the registers to two blocks a wave: 8192 of 8192 240 ->
+  // 233 us, of 5120 159 -> 146.
+  if (!BRANCH && nblocks <= 8 && a.M > 3 * dev.cu_count)
+    return launch_form<2, ROT, BRANCH, false, 256, 3>(a, dev, stream);
+  if (nblocks <= 16) return launch_form<1, ROT, BRANCH, true, 1024, 4>(a, dev, stream);
+  // two up to 24 (17408: one token 9.6 us, 2048 109; four a wave 14.5 and 149), then
+  // four, in more registers (28672: 98 us against 106) while 12 waves hold the row
   if (nblocks <= 24) return launch_form<2, ROT, BRANCH, false, 768, 3>(a, dev, stream);
   if (nblocks <= 48) return launch_form<4, ROT, BRANCH, false, 768, 3>(a, dev, stream);
   return launch_form<4, ROT, BRANCH, false, 1024, 4>(a, dev, stream);

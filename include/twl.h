@@ -361,7 +361,8 @@ twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual
  * TWL_LORA_MAX_R (pad A and B with zeros for other ranks); N at most 2^22; a
  * kind other than the two, or an output overlapping an input (other than
  * out == y), is TWL_EINVAL.  n_adapters = 0 copies y.  Values that are not finite
- * in one adapter or token reach only the tokens that use it.
+ * in one adapter or token make results not finite (infinities may become NaN) of
+ * the tokens that use it only.
  */
 #define TWL_LORA_MAX_R 128
 twl_status twl_lora_add(const void* y, const uint16_t* x, const int32_t* ids, const uint16_t* lora_a,
@@ -403,7 +404,8 @@ twl_status twl_pack_ternary_gated(const int8_t* code_gate, const uint16_t* s_gat
  *   workspace: twl_gated_workspace_bytes(M, N, K) bytes (covers every path),
  *             contents on entry do not matter; calls sharing one must not run
  *             concurrently
- * N is at most 2^29.  Other errors as ternary_linear_ex.
+ * N is at most 2^29; an output that overlaps an input or the workspace is
+ * TWL_EINVAL.  Other errors as ternary_linear_ex.
  */
 twl_status twl_ternary_gated_linear(const int8_t* x_i8, const float* a_scale, const uint8_t* packed,
                                     const int8_t* q, const float* smax, int64_t M, int64_t N,

@@ -1,9 +1,10 @@
 """The operators of the block around the ternary linear layer: Python binding of
 their entry points in include/twl.h (argument checks and marshalling only).
 
-Tensors must be contiguous CUDA (HIP) tensors on the current device; bf16
-arguments may also be given as their int16 bit patterns.  Outputs and workspaces
-that a call allocates belong to the stream the call runs on.
+Tensors must be contiguous CUDA (HIP) tensors on the current device (but for
+the rows of norm_rotate_quant_act's gate); bf16 arguments may also be given as
+their int16 bit patterns.  Outputs and workspaces that a call allocates belong to
+the stream the call runs on.
 """
 from __future__ import annotations
 
@@ -59,6 +60,14 @@ def _check(t, name, shape, dtypes, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _check_rows(t, name, shape, dtypes, device):
+    """As _check for a matrix whose rows may lie apart or, with stride 0, be one row
+    for all: pointer and distance of the rows in elements."""
+    if t.is_contiguous() or t.shape != shape or t.stride(1) != 1:
+        return _check(t, name, shape, dtypes, device), shape[1]
+    return _check(t[0], name, shape[1:], dtypes, device), t.stride(0)
+
+
 def _matrix(t, name):
     """The sizes of a two-dimensional tensor argument."""
     try:
@@ -108,11 +117,12 @@ def norm_rotate_quant_act(x, weight, sign, eps=1e-6, residual=None, post_weight=
     rotate_quant_act(normed, sign).
 
     x and residual [M, K] bf16, weights [K] bf16, sign [K] int8 (None: no
-    rotation).  Returns (x_i8, a_scale, h, normed): h is None when nothing
-    changes x (no residual, post_weight, gate or branch_scale), normed unless
-    return_normed, x_i8 and a_scale without sign.  Buffers given for the outputs
-    are written and returned; h may be x or residual itself.  return_normed, or
-    normed=, is required without sign."""
+    rotation).  The rows of a gate [M, K] may lie a multiple of 8 elements apart
+    (a slice of a wider tensor) or be one row expanded.  Returns (x_i8, a_scale,
+    h, normed): h is None when nothing changes x (no residual, post_weight, gate
+    or branch_scale), normed unless return_normed, x_i8 and a_scale without sign.
+    Buffers given for the outputs are written and returned; h may be x or residual
+    itself.  return_normed, or normed=, is required without sign."""
     env = _env()
     device = env.device()
     M, K = _matrix(x, "x")
@@ -126,8 +136,10 @@ def norm_rotate_quant_act(x, weight, sign, eps=1e-6, residual=None, post_weight=
     if post_weight is not None:
         p_post = _check(post_weight, "post_weight", row, bf16, device)
     if gate is not None:
-        gate_stride = K if len(getattr(gate, "shape", ())) == 2 else 0
-        p_gate = _check(gate, "gate", wide if gate_stride else row, bf16, device)
+        if len(getattr(gate, "shape", ())) == 2:
+            p_gate, gate_stride = _check_rows(gate, "gate", wide, bf16, device)
+        else:
+            p_gate = _check(gate, "gate", row, bf16, device)
     if sign is not None:
         p_sign = _check(sign, "sign", row, env.int8, device)
         if x_i8 is None:

@@ -111,10 +111,18 @@ twl_status twl_ternary_gated_linear(const int8_t* x_i8, const float* a_scale, co
   TWL_REQUIRE_PTR(q);
   TWL_REQUIRE_PTR(smax);
   TWL_REQUIRE_PTR(out);
+  const size_t rows = static_cast<size_t>(M), n2 = 2 * static_cast<size_t>(N), k = static_cast<size_t>(K);
+  const Range in[] = {{x_i8, rows * k, "x_i8"}, {a_scale, rows * 4, "a_scale"}, {packed, (n2 + 63) / 64 * 64 * (k / 4), "packed"},
+                      {q, n2 * (k / 128), "q"}, {smax, n2 * 4, "smax"}, {out, rows * N * (out_kind == TWL_OUT_F32 ? 4 : 2), "out"}};
+  for (int i = 0; i < 5; ++i)
+    if (overlap(in[5], in[i])) return fail(TWL_EINVAL, "out overlaps %s", in[i].name);
   twl::DeviceInfo dev;
   TWL_TRY(current_device(&dev));
   const size_t need = gated_need(M, N, K, path, dev);
   TWL_TRY(check_workspace(need, workspace, workspace_bytes));
+  const Range scratch = {need > 0 ? workspace : nullptr, need, "workspace"};
+  for (const Range& i : in)
+    if (overlap(scratch, i)) return fail(TWL_EINVAL, "workspace overlaps %s", i.name);
   const twl::OutKind kind = out_kind == TWL_OUT_BF16 ? twl::kOutGatedBf16 : twl::kOutGatedF32;
   if (gated_decodes(M, path))
     return launched(twl::launch_gemv_gated(x_i8, a_scale, packed, q, smax, M, 2 * N, K, out, kind, workspace, dev, stream),

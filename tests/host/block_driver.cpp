@@ -161,6 +161,9 @@ int main() {
   CHECK(gated(4, TWL_PATH_GEMM, TWL_OUT_F32, u16(P(6)), 1000) == TWL_OK && !g_decode && g_kind == twl::kOutGatedF32);
   CHECK(gated(25, TWL_PATH_AUTO, TWL_OUT_F32, u16(P(6)), 1000) == TWL_OK && !g_decode && g_n == 200);
   CHECK(gated(25, TWL_PATH_GEMV, TWL_OUT_F32, u16(P(6)), 4000) == TWL_ESHAPE);
+  CHECK(gated(4, 0, TWL_OUT_F32, u16(P(2) + 50 * 1024), 4000) == TWL_EINVAL);  // over the last packed rows: 256 x K / 4
+  CHECK(gated(4, 0, TWL_OUT_F32, u16(P(2) + 64 * 1024), 4000) == TWL_OK);
+  CHECK(gated(4, 0, TWL_OUT_F32, u16(P(5) + 1584), 4000) == TWL_EINVAL);  // over out's end
   CHECK(gated(4, TWL_PATH_GEMV_MFMA, TWL_OUT_F32, u16(P(6)), 4000) == TWL_EINVAL);
   g_launch = hipErrorInvalidConfiguration;
   CHECK(gated(4, 0, TWL_OUT_F32, u16(P(6)), 4000) == TWL_EHIP);

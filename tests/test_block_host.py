@@ -148,6 +148,10 @@ def _gated(lib, **kw):
     (dict(smax=None), EINVAL, b"smax is NULL"),
     (dict(out=None), EINVAL, b"out is NULL"),
     (dict(out=P[5] + 8), EALIGN, b"out is not"),
+    (dict(out=P[0] + 4080), EINVAL, b"out overlaps x_i8"),
+    (dict(out=P[2] - 512 + 16), EINVAL, b"out overlaps packed"),
+    (dict(out=P[3] + 1008), EINVAL, b"out overlaps q"),
+    (dict(out=P[4]), EINVAL, b"out overlaps smax"),
 ])
 def test_gated_refuses(lib, kw, status, word):
     assert _gated(lib, **kw) == status

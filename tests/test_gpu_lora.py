@@ -84,6 +84,13 @@ BF, F32 = torch.bfloat16, torch.float32
     (300, 16501, 256, 96, 9, mixed),
     (130, 32768, 128, 128, 2, runs),
     (128, 33000, 128, 64, 3, mixed),
+    (256, 72, 512, 40, 20, mixed),
+    (257, 72, 512, 40, 20, mixed),
+    (700, 1032, 512, 128, 20, mixed),
+    (1030, 264, 512, 64, 5, runs),
+    (1040, 77, 256, 8, 3, runs),
+    (1100, 136, 256, 32, 40, mixed),
+    (1025, 16392, 128, 24, 6, runs),
 ])
 def test_values(twl, M, N, K, R, n, ids, dtype):
     announce(f"lora M={M} N={N} K={K} R={R} n={n} {dtype}")

@@ -86,6 +86,34 @@ def test_widths(twl, M, K):
     _check(_run(twl, c), c)
 
 
+# more tokens than run at once, in both splits of the row, and three rows a workgroup
+@pytest.mark.parametrize("M,K,branch", [
+    (800, 2048, False), (1100, 5120, False), (770, 8192, False), (800, 5120, True), (600, 9216, True), (300, 16384, False),
+    (300, 16384, True), (1600, 7168, True), (260, 12288, False)])
+def test_many_tokens(twl, M, K, branch):
+    announce(f"norm M={M} K={K} branch={branch}")
+    c = _case(M + K + 1, M, K, branch, branch, "token" if branch else "none")
+    _check(_run(twl, c), c)
+
+
+def test_gate_rows_apart_and_expanded(twl):
+    """A gate whose rows lie apart (a slice of a wider tensor), one row expanded,
+    and strides that are refused."""
+    M, K = 6, 1024
+    c = _case(14, M, K, True, True, "token")
+    wide = torch.zeros((M, 3 * K + 8), dtype=torch.int16, device="cuda")
+    wide[:, K + 8:2 * K + 8] = _t(c["gate_bits"])
+    announce("norm gate rows apart")
+    _check(_run(twl, c, gate=wide[:, K + 8:2 * K + 8]), c)
+    announce("norm gate row expanded")
+    one = _t(c["gate_bits"])[:1].expand(M, K)
+    _check(_run(twl, c, gate=one), dict(c, gate_bits=np.repeat(c["gate_bits"][:1], M, 0)))
+    for bad in (wide[:, :2 * K:2], wide[:, 1:K + 1], torch.zeros((M, K + 4), dtype=torch.int16, device="cuda")[:, :K],
+                torch.zeros(M * K, dtype=torch.int16, device="cuda").as_strided((M, K), (8, 1))):
+        with pytest.raises((ValueError, twl.TwlError)):
+            _run(twl, c, gate=bad)
+
+
 def test_without_rotation(twl):
     for M, K in ((1, 1024), (700, 2048), (2, 33792)):
         announce(f"norm only M={M} K={K}")

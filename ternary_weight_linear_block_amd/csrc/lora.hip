@@ -103,8 +103,7 @@ __global__ __launch_bounds__(64 * shrink_waves(TS)) void lora_shrink_kernel(Lora
   constexpr int TM = 16 * TS;
   constexpr int kStride = 16 * RT + 4;  // floats of a token's row of sums, padded
   constexpr int G = 2 * (TS + RT);      // groups of 8 rows: x, then A
-  constexpr int U = G <= 6 ? 2 : 1;     // 64-k units loaded together
-  constexpr int kStage = U * G * 1024, kSums = TM * kStride * 4;
+  constexpr int kStage = G * 1024, kSums = TM * kStride * 4;
   __shared__ __attribute__((aligned(16))) char lds[kShrinkWaves * (kStage > kSums ? kStage : kSums)];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -131,18 +130,16 @@ __global__ __launch_bounds__(64 * shrink_waves(TS)) void lora_shrink_kernel(Lora
     off[g] = static_cast<uint32_t>(r) * static_cast<uint32_t>(2 * K) + 16 * c8;
   }
   const int put = r8 * 128 + 16 * (c8 ^ r8);
-  const auto get = [&](int u, int frag, int s) {  // fragment frag (x, then A), k step s of unit u
-    const int at = (u * G + 2 * frag + (j >> 3)) * 1024 + (j & 7) * 128 + 16 * ((4 * s + q) ^ (j & 7));
+  const auto get = [&](int frag, int s) {  // fragment frag (x, then A), k step s of the unit
+    const int at = (2 * frag + (j >> 3)) * 1024 + (j & 7) * 128 + 16 * ((4 * s + q) ^ (j & 7));
     return *reinterpret_cast<const v8bf*>(stage + at);
   };
 
-  v4u raw[U][G];
-  const auto load = [&](int g0, int g1, const char* base, int u) {  // units past the last re-read it and are not multiplied
+  v4u raw[G];
+  const auto load = [&](int g0, int g1, const char* base, int u) {  // a unit past the last re-reads it and is not multiplied
 #pragma unroll
-    for (int v = 0; v < U; ++v)
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-        if (g >= g0 && g < g1) raw[v][g] = *reinterpret_cast<const v4u*>(base + off[g] + 128 * max(min(u + v, u1 - 1), 0));
+    for (int g = 0; g < G; ++g)
+      if (g >= g0 && g < g1) raw[g] = *reinterpret_cast<const v4u*>(base + off[g] + 128 * max(min(u, u1 - 1), 0));
   };
   constexpr int kAll = 2 * TS;  // groups of x
   Passes passes(a.ids, t0, TM, a.M, a.n, lane);
@@ -159,29 +156,23 @@ __global__ __launch_bounds__(64 * shrink_waves(TS)) void lora_shrink_kernel(Lora
       for (int f = 0; f < RT; ++f) acc[h][f] = v4f{0};
     load(0, kAll, xb, u0);
     load(kAll, G, ab, u0);
-    for (int u = u0; u < u1; u += U) {
-      wave_lds_sync();  // the previous units have been read
+    for (int u = u0; u < u1; ++u) {
+      wave_lds_sync();  // the previous unit has been read
 #pragma unroll
-      for (int v = 0; v < U; ++v)
-#pragma unroll
-        for (int g = 0; g < G; ++g) *reinterpret_cast<v4u*>(stage + (v * G + g) * 1024 + put) = raw[v][g];
-      load(0, kAll, xb, u + U);
-      load(kAll, G, ab, u + U);
+      for (int g = 0; g < G; ++g) *reinterpret_cast<v4u*>(stage + g * 1024 + put) = raw[g];
+      load(0, kAll, xb, u + 1);
+      load(kAll, G, ab, u + 1);
       wave_lds_sync();
 #pragma unroll
-      for (int v = 0; v < U; ++v) {
-        if (u + v >= u1) break;
+      for (int s = 0; s < 2; ++s) {
+        v8bf xv[TS];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          v8bf xv[TS];
+        for (int h = 0; h < TS; ++h) xv[h] = get(h, s);
 #pragma unroll
-          for (int h = 0; h < TS; ++h) xv[h] = get(v, h, s);
+        for (int f = 0; f < RT; ++f) {
+          const v8bf av = get(TS + f, s);
 #pragma unroll
-          for (int f = 0; f < RT; ++f) {
-            const v8bf av = get(v, TS + f, s);
-#pragma unroll
-            for (int h = 0; h < TS; ++h) acc[h][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xv[h], acc[h][f], 0, 0, 0);
-          }
+          for (int h = 0; h < TS; ++h) acc[h][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xv[h], acc[h][f], 0, 0, 0);
         }
       }
     }

@@ -11,6 +11,11 @@
 // formed there, in the same launch.  Layers too narrow for it run the linear
 // layer's dot4 or K-split kernel up to its int32 partial sums and the finishing
 // kernel below, which takes the place of its reduce kernel.
+//
+// 2 x 17408 x 5120: 12 us for one token (46 MB, 3.9 TB/s, what the row-balanced
+// kernel reaches for the plain layer of as many rows) and 16.7 us for 24, bound by
+// the stream of the weights and, with 24 tokens, by the MFMA and LDS work of the
+// two token tiles.
 #include "gemv_rows.h"
 
 #include <cstdio>

@@ -33,7 +33,10 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
-constexpr int shrink_waves(int ts) { return ts == 1 ? 8 : 4; }  // with 32 tokens, LDS for three workgroups a CU
+// With 32 tokens four waves, whose LDS leaves three workgroups a CU (eight: 4096
+// tokens of rank 64 117 us instead of 110); with 16 eight, each with less of K (500
+// tokens of K = 17408 25.3 us, four 26.7; 1000 tokens of rank 16 17.5 and 16.3).
+constexpr int shrink_waves(int ts) { return ts == 1 ? 8 : 4; }
 constexpr int kExpandWaves = 4;
 constexpr int kLdsBytes = 160 * 1024;  // of a CU
 
@@ -61,9 +64,11 @@ struct Passes {
   }
 };
 
-// Workgroups are dispatched to the XCDs in turn: work item of workgroup `bid` of `total` such
-// that each XCD gets a contiguous range of the items, whose neighbours share an
-// adapter's rows in its L2.
+// Workgroups are dispatched to the XCDs in turn: work item of workgroup `bid` of
+// `total` such that each XCD gets a contiguous range of the items, whose neighbours
+// share an adapter's rows in its L2 (4096 tokens of rank 64 on 17408: 110 us, with
+// the items in order 126).  Workgroups of later passes stand behind all of the first
+// passes', so that those without a pass cost little (between them: 135 against 114).
 __device__ __forceinline__ int xcd_item(int bid, int total) {
   constexpr int kXcds = 8;
   const int per = total / kXcds, rem = total % kXcds, xcd = bid % kXcds;
@@ -88,15 +93,22 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Work item (slice, tile, p): passes p, p + passes, ... of 16 TS tokens over one
+// Work item (p, slice, tile): passes p, p + passes, ... of 16 TS tokens over one
 // slice of K.  RT: 16-row fragments of the rank.
 //
 // A load straight into the operand's layout (lane = 16 bytes of one of 16 rows)
 // touches 64 cache lines an instruction, and the address unit bounds the kernel
-// (4096 tokens of 5120, rank 64: 54 us).  So a wave loads 64 k of its rows with 8
+// (4096 tokens of 5120, rank 64: 59 us).  So a wave loads 64 k of its rows with 8
 // lanes a row and 8 rows an instruction, and turns them over in LDS of its own
 // (16-byte units swizzled by row, no bank conflicts): no barrier before the sums
-// meet.
+// meet.  The next 64 k are on their way while these are multiplied; two units at
+// once cost the LDS of other workgroups (200 tokens of 32 adapters, rank 16, both
+// kernels: 23.4 against 20.5 us).
+//
+// 25 us for 4096 tokens of 5120 and rank 64, 1.7 TB/s of x: still the address unit
+// (half of the time busy), which A passes through once for 32 tokens; 13 us for 500
+// tokens of 17408, 2.7 TB/s of x and A; 3.8 us for one token, the latency of ids,
+// operands and sums in turn.
 template <int RT, int TS>
 __global__ __launch_bounds__(64 * shrink_waves(TS)) void lora_shrink_kernel(LoraArgs a) {
   constexpr int kShrinkWaves = shrink_waves(TS);
@@ -198,8 +210,8 @@ __global__ __launch_bounds__(64 * shrink_waves(TS)) void lora_shrink_kernel(Lora
 
 // Loads and stores through a buffer resource: a lane whose offset is kOutside reads
 // zeros and writes nothing, so no branch stands around them (behind a branch the
-// compiler cannot count what is in flight and waits for all of it: 115 us for 4096
-// tokens of rank 64 on 17408, bf16).  Ranges stay below 2^31 bytes.
+// compiler cannot count what is in flight and waits for all of it).  Ranges stay
+// below 2^31 bytes.
 constexpr int kRawBufferWord3 = 0x00020000;  // 32-bit data format, no swizzle: a byte count as range
 constexpr uint32_t kOutside = 0x80000000u;
 
@@ -267,17 +279,21 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Work item (chunk, tile, p): passes p, p + passes, ... of 16 WT tokens over an even
+// Work item (p, chunk, tile): passes p, p + passes, ... of 16 WT tokens over an even
 // share of the ranges of 64 WN n, WN = 4 / WT.  A wave has 16 tokens x 64 n: with
 // WT = 4 the waves share B's 64 rows, with WT = 1 (few tokens) each has its own.
 // RS: 32-rank steps.
 //
 // As in the shrink kernel nothing is read or written in the matrix layout, whose
-// lanes lie a row of y apart (measured with it: 145 us for 4096 tokens of rank 64
-// on 17408, bf16): B's 64 rows are one piece of memory, copied to LDS in order, and
-// the products go through LDS to where y's 16-byte pieces are.  v stays in
-// registers; the next range's B and the next two's y are on their way while one is
-// computed.
+// lanes lie a row of y apart: B's 64 rows are one piece of memory, copied to LDS in
+// order, and the products go through LDS to where y's 16-byte pieces are.  v stays
+// in registers; the next range's B and the next two's y are on their way while one
+// is computed.
+//
+// 85 us for 4096 tokens of rank 64 on 17408, bf16: 3.4 TB/s of y in and out, and as
+// many bytes of B from L2 again; what is left is the wait for ids, partial sums and
+// first operands (16 us when no second pass runs beside them).  8 us for 24 tokens
+// of as many adapters, rank 16: 2 TB/s of B, two latencies more than a copy.
 constexpr int kOutStride = 64 + 4;  // floats of a token's products in LDS, padded
 
 struct ExpandLds {
@@ -508,8 +524,12 @@ int passes_of(int64_t M, int n, int tokens) {
 }
 
 // Tiles of 32 tokens (each row of A read once for two fragments of tokens) where
-// there are enough of them and the ranks' rows leave LDS for it, and slices of K
-// that give every CU a workgroup, a wave at least one 64-k unit.
+// there are enough of them and the ranks' rows leave LDS for it: 4096 tokens of rank
+// 64 110 us, in tiles of 16 122; 1000 tokens 44 and 38.  Slices of K that give every
+// CU a workgroup (two of the smaller ones of 32 tokens), a wave at least one 64-k
+// unit: half as many take 118 us for 4096 tokens and 31 instead of 25 for 500 of
+// K = 17408, twice as many 114 and 31, for their sums are read again in every range
+// of n.
 void plan_shrink(LoraArgs& a, const DeviceInfo& dev) {
   const int cus = std::max(1, dev.cu_count);
   a.shrink_ts = a.M > 4 * static_cast<int64_t>(cus) && a.R <= 64 ? 2 : 1;

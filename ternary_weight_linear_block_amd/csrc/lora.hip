@@ -293,7 +293,7 @@ __device__ __forceinline__ void lds_barrier() {
 // 85 us for 4096 tokens of rank 64 on 17408, bf16: 3.4 TB/s of y in and out, and as
 // many bytes of B from L2 again; what is left is the wait for ids, partial sums and
 // first operands (16 us when no second pass runs beside them).  8 us for 24 tokens
-// of as many adapters, rank 16: 2 TB/s of B, two latencies more than a copy.
+// of as many adapters, rank 16: 1.6 TB/s of B, two latencies more than a copy.
 constexpr int kOutStride = 64 + 4;  // floats of a token's products in LDS, padded
 
 struct ExpandLds {
@@ -517,10 +517,14 @@ constexpr int kSplitPassesM = 256;
 // Workgroups that share a tile's passes (pass p, p + passes, ...).  Larger batches
 // have few adapters a tile, and a workgroup without a pass costs its launch: 4096
 // tokens of 24 requests take 109 us with four, 127 with one (a tile in which one
-// request ends and the next begins takes twice as long) and 117 with 16; 1500
-// tokens of 16 adapters in any order 119, and 136 with two.
-int passes_of(int64_t M, int n, int tokens) {
-  return static_cast<int>(std::min<int64_t>({M <= kSplitPassesM ? 16 : 4, M, std::max(1, n), tokens}));
+// request ends and the next begins takes twice as long); 1500 tokens of 16 adapters
+// in any order 112, and 136 with two; but 1000 tokens of rank 16 17 us with four and
+// 21.5 with eight.  Eight cost nothing where y is large (from 4 x 10^7 elements on:
+// the 4096 tokens above 109, and 337 instead of 500 us with 200 of them in decode,
+// each with an adapter of its own).
+int passes_of(const LoraArgs& a, int tokens) {
+  const int share = a.M <= kSplitPassesM ? 16 : a.M * a.N >= 40000000 ? 8 : 4;
+  return static_cast<int>(std::min<int64_t>({share, a.M, std::max(1, a.n), tokens}));
 }
 
 // Tiles of 32 tokens (each row of A read once for two fragments of tokens) where
@@ -534,7 +538,7 @@ void plan_shrink(LoraArgs& a, const DeviceInfo& dev) {
   const int cus = std::max(1, dev.cu_count);
   a.shrink_ts = a.M > 4 * static_cast<int64_t>(cus) && a.R <= 64 ? 2 : 1;
   a.shrink_tiles = ceil_div(a.M, 16 * a.shrink_ts);
-  a.shrink_passes = passes_of(a.M, a.n, 16 * a.shrink_ts);
+  a.shrink_passes = passes_of(a, 16 * a.shrink_ts);
   const int64_t busy = a.M <= kSplitPassesM ? std::min<int64_t>(a.M, std::max(1, a.n)) : a.shrink_tiles;
   const int64_t want = a.shrink_ts == 1 ? cus : 2 * cus;
   a.slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((want + busy - 1) / busy, a.K / 64 / shrink_waves(a.shrink_ts))));
@@ -578,7 +582,7 @@ hipError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo& dev, hipStream_t
   const int WT = a.M > kSplitPassesM && large ? 4 : 1;
   const int RS = a.R <= 32 ? 1 : a.R <= 64 ? 2 : 4;
   a.expand_tiles = ceil_div(a.M, 16 * WT);
-  a.expand_passes = passes_of(a.M, a.n, 16 * WT);
+  a.expand_passes = passes_of(a, 16 * WT);
   // Ranges of n a workgroup.  Each workgroup sums the slices of its tokens and waits
   // for its first operands, so few long ones are better, as long as they fill the
   // card: first passes take half of the workgroups that can be resident (the other

@@ -331,7 +331,8 @@ int twl_rotate_quant_linear_fused(int64_t M, int64_t N, int64_t K);
  *   x_i8        out: int8 [M, K];  a_scale out: fp32 [M]  (NULL when sign is)
  * eps must be positive.  Outputs that overlap an input (other than h) or each
  * other are TWL_EINVAL.  A row whose values are not finite gives unspecified
- * results in that row only.
+ * results in that row only.  A product x * post_weight * gate or h * weight below
+ * 2^-126 is rounded to a multiple of 2^-149 before the norm's factor.
  */
 twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual,
                                      const uint16_t* post_weight, const uint16_t* gate,

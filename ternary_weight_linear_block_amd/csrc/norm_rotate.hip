@@ -370,7 +370,7 @@ void norm_rotate_kernel(NormArgs a) {
       if (tq.markstein)
         store_all([&](float w) { return rot::quotient_markstein(w, tq); });
       else
-        store_all([&](float w) { return w / tq.div; });
+        store_all([&](float w) { return rot::quotient_unscaled(w, tq); });
     }
   }
 }

@@ -245,12 +245,19 @@ __device__ __forceinline__ TokenQuant token_quant(float absmax) {
 
 // The quantiser for values 32 r of rotate_loaded<., false>, given their absmax: the
 // scale of r itself, and divisor and reciprocal for 32 r.  Every quotient is that of
-// r and the scale to the bit (multiplying by 32 rounds nothing).
+// r and the scale to the bit: multiplying by 32 rounds nothing, and where dividing by
+// it does (r below 2^-126) r is far below half a scale of 2^-64, or the quotient is
+// quotient_unscaled's.
 __device__ __forceinline__ TokenQuant token_quant_unscaled(float absmax32) {
   TokenQuant t = token_quant(absmax32 * 0.03125f);
   t.div *= 32.0f;
   t.inv *= 0.03125f;
   return t;
+}
+
+// The quotient of a small scale (no markstein) for 32 r: of r, rounded as in memory.
+__device__ __forceinline__ float quotient_unscaled(float w, const TokenQuant& t) {
+  return w * 0.03125f / (t.div * 0.03125f);
 }
 
 // rint and clamp of a quotient, as the int8 byte

@@ -145,6 +145,17 @@ def test_extreme_rows(twl):
     assert not host(got[0])[0].any() and host(got[1])[0] == 0.0
 
 
+@pytest.mark.parametrize("weight", [2e-38, 3e-37, 1e-34, 1e-22, 1e-18])
+def test_small_weights(twl, weight):
+    """Rotated values and scales that are denormal, and either side of the quantiser's
+    division."""
+    for M, K, branch in ((3, 1024, True), (800, 2048, False)):
+        c = _case(17, M, K, branch, branch, "none")
+        c["weight_bits"] = W.f32_to_bf16_bits((weight * (1 + 0.2 * np.random.default_rng(3).standard_normal(K))).astype(np.float32))
+        announce(f"norm weight={weight} M={M}")
+        _check(_run(twl, c), c)
+
+
 def test_outputs_in_place_and_given(twl):
     c = _case(3, 9, 5120, True, True, "none")
     x, r = _t(c["x_bits"]), _t(c["residual_bits"])

@@ -346,8 +346,9 @@ twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual
  *   v[t,r]   = sum_k x[t,k] A[i,r,k]          with i = ids[t]
  *   out[t,n] = y[t,n] + scale[i] sum_r v[t,r] B[i,n,r]
  * A token whose id is outside 0 .. n_adapters-1 (-1, say) has no adapter:
- * out[t] = y[t].  Sums are fp32; v enters the second product as two bf16 terms
- * (three for fp32 y), i.e. to 2^-16 (2^-24) of its value; out is rounded once.
+ * out[t] = y[t].  Sums are fp32; v enters the second product in fp32 or as two
+ * bf16 terms (three for fp32 y), i.e. to 2^-16 (2^-24) of its value; out is rounded
+ * once.
  * Tokens of one adapter need not be adjacent; adjacent ones are faster.
  *   y     in : [M, N] of the kind (TWL_OUT_F32 or TWL_OUT_BF16)
  *   x     in : bf16 bit patterns [M, K], the projection's input before rotation

@@ -5,9 +5,11 @@
 //   v[t, r]   = sum_k x[t, k] A[a, r, k]
 //   out[t, n] = y[t, n] + sum_r (scale[a] v[t, r]) B[a, n, r]
 //
-// Two kernels, both on v_mfma_f32_16x16x32_bf16 with the adapter's rows as the
-// first operand and 16 tokens as the second, so that a lane's results are
-// consecutive ranks (or n) of one token:
+// A decode batch of small adapters takes one kernel, a token and a share of n to a
+// workgroup (lora_token_kernel).  All else takes two, both on
+// v_mfma_f32_16x16x32_bf16 with the adapter's rows as the first operand and 16
+// tokens as the second, so that a lane's results are consecutive ranks (or n) of one
+// token:
 //   shrink  a workgroup takes 16 consecutive tokens and a slice of K, its waves
 //           split the slice; their sums meet in LDS (in wave order) and the slice's
 //           sum goes to the workspace, fp32 [slices][M][R].
@@ -102,13 +104,12 @@ __device__ __forceinline__ void wave_lds_sync() {
 // lanes a row and 8 rows an instruction, and turns them over in LDS of its own
 // (16-byte units swizzled by row, no bank conflicts): no barrier before the sums
 // meet.  The next 64 k are on their way while these are multiplied; two units at
-// once cost the LDS of other workgroups (200 tokens of 32 adapters, rank 16, both
-// kernels: 23.4 against 20.5 us).
+// once cost the LDS of other workgroups (400 tokens of 16 adapters, rank 16, both
+// kernels: 41.5 against 36.3 us).
 //
 // 25 us for 4096 tokens of 5120 and rank 64, 1.7 TB/s of x: still the address unit
 // (half of the time busy), which A passes through once for 32 tokens; 13 us for 500
-// tokens of 17408, 2.7 TB/s of x and A; 3.8 us for one token, the latency of ids,
-// operands and sums in turn.
+// tokens of 17408, 2.7 TB/s of x and A.
 template <int RT, int TS>
 __global__ __launch_bounds__(64 * shrink_waves(TS)) void lora_shrink_kernel(LoraArgs a) {
   constexpr int kShrinkWaves = shrink_waves(TS);
@@ -292,8 +293,7 @@ __device__ __forceinline__ void lds_barrier() {
 //
 // 85 us for 4096 tokens of rank 64 on 17408, bf16: 3.4 TB/s of y in and out, and as
 // many bytes of B from L2 again; what is left is the wait for ids, partial sums and
-// first operands (16 us when no second pass runs beside them).  8 us for 24 tokens
-// of as many adapters, rank 16: 1.6 TB/s of B, two latencies more than a copy.
+// first operands (16 us when no second pass runs beside them).
 constexpr int kOutStride = 64 + 4;  // floats of a token's products in LDS, padded
 
 struct ExpandLds {
@@ -495,6 +495,141 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
   }
 }
 
+// Decode: both products of one token over one share of n, in one launch.
+//
+// A workgroup computes all of its token's v: thread = 8 k of every row of A, eight
+// rows in flight and the next eight behind them, fp32 sums by v_dot2_f32_bf16, lanes
+// by rotations, waves in LDS in order.  Then thread = one n: R products with v in
+// fp32.  Every workgroup of a token reads its A again (from L2), which costs less
+// than a second launch and its latencies as long as A is small.
+//
+// 6.8 us for one token of rank 16 on 5120 x 5120 (two kernels: 8.0), 9.3 us for 24
+// tokens of 32 adapters on 5120 x 17408 (12.0): ids, A, the sums and B in turn, and
+// 1 us at least for each eight rows.
+constexpr int kTokenThreads = 1024;
+constexpr int kTokenSteps = 3;             // of eight rows of 8192 k
+constexpr int kTokenR = 8 * kTokenSteps;   // largest rank
+
+__device__ __forceinline__ float add_row16(float s) {  // sum over 16 lanes, in all of them
+  s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0x128, 0xF, 0xF, true));
+  s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0x124, 0xF, 0xF, true));
+  s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0x122, 0xF, 0xF, true));
+  s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0x121, 0xF, 0xF, true));
+  return s;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_y(const void* y, size_t at) {
+  if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(y)[at]) << 16);
+  else return static_cast<const float*>(y)[at];
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_y(void* out, size_t at, float v) {
+  if constexpr (BF16) static_cast<uint16_t*>(out)[at] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
+  else static_cast<float*>(out)[at] = v;
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kTokenThreads) void lora_token_kernel(LoraArgs a) {
+  constexpr int kGroups = kTokenThreads / 16;  // of lanes whose sums meet in LDS
+  __shared__ float part[kTokenR][kGroups + 1];
+  __shared__ __attribute__((aligned(16))) float v_lds[kTokenR];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const uint32_t item = xcd_item(blockIdx.x, gridDim.x);
+  const uint32_t t = item / a.expand_chunks, chunk = item - t * a.expand_chunks;
+  const int N = a.N, K = a.K, R = a.R;
+  const int units = (N + 63) / 64;
+  const int n_lo = 64 * static_cast<int>(static_cast<int64_t>(units) * chunk / a.expand_chunks);
+  const int n_hi = min(N, 64 * static_cast<int>(static_cast<int64_t>(units) * (chunk + 1) / a.expand_chunks));
+  const size_t row = static_cast<size_t>(t) * N;
+  const int n0 = min(n_lo + tid, N - 1);
+  const float y0 = load_y<BF16>(a.y, row + n0);
+  const int id = __builtin_amdgcn_readfirstlane(a.ids[t]);
+  if (id < 0 || id >= a.n) {
+    if (a.out == a.y) return;
+    for (int n = n_lo + tid; n < n_hi; n += kTokenThreads) store_y<BF16>(a.out, row + n, load_y<BF16>(a.y, row + n));
+    return;
+  }
+  const uint16_t* b = a.b + static_cast<size_t>(id) * N * R;
+  const uint16_t* at = a.a + static_cast<size_t>(id) * R * K;
+  const uint16_t* x = a.x + static_cast<size_t>(t) * K;
+  const int pieces = K / 8, rounds = (pieces + kTokenThreads - 1) / kTokenThreads;
+  const float scale = a.scale[id];
+
+  // eight rows of A and x at this thread's piece; a piece past the end is zeros of x
+  struct Step {
+    v4u a[8], x;
+  };
+  const auto load = [&](Step& s, int r0, int round) {
+    const int p = tid + round * kTokenThreads, k = 8 * min(p, pieces - 1);
+    s.x = *reinterpret_cast<const v4u*>(x + k);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) s.a[r] = *reinterpret_cast<const v4u*>(at + static_cast<size_t>(min(r0 + r, R - 1)) * K + k);
+    if (p >= pieces) s.x = v4u{0, 0, 0, 0};
+  };
+  Step cur, next;
+  load(cur, 0, 0);
+  v4u b0[kTokenSteps];  // the first n's row of B
+#pragma unroll
+  for (int p = 0; p < kTokenSteps; ++p) b0[p] = *reinterpret_cast<const v4u*>(b + static_cast<size_t>(n0) * R + 8 * min(p, R / 8 - 1));
+  float acc[8] = {};
+  int r0 = 0, round = 0;
+  const int steps = (R / 8) * rounds;
+  for (int i = 0; i < steps; ++i) {
+    const bool last = round + 1 == rounds;
+    const int rn = last ? r0 + 8 : r0, roundn = last ? 0 : round + 1;
+    load(next, rn, roundn);
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = cur.a[r][e], v = cur.x[e];  // a bit_cast of the elements themselves takes the first
+        acc[r] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, w), __builtin_bit_cast(v2bf, v), acc[r], false);
+      }
+    if (last) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float s = add_row16(acc[r]);
+        if ((lane & 15) == 0) part[r0 + r][tid >> 4] = s;
+        acc[r] = 0.0f;
+      }
+    }
+    cur = next;
+    r0 = rn;
+    round = roundn;
+  }
+  __syncthreads();
+  if (tid < 8 * R) {
+    const int r = tid >> 3, g = tid & 7;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGroups / 8; ++i) s += part[r][8 * i + g];
+    s += __shfl_xor(s, 1);
+    s += __shfl_xor(s, 2);
+    s += __shfl_xor(s, 4);
+    if (g == 0) v_lds[r] = scale * s;
+  }
+  __syncthreads();
+  for (int n = n_lo + tid; n < n_hi; n += kTokenThreads) {
+    const bool ahead = n == n_lo + tid;
+    float s = 0.0f;
+    const auto add = [&](const v4u& w, int p) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = __builtin_fmaf(v_lds[8 * p + 2 * e], __uint_as_float(w[e] << 16), s);
+        s = __builtin_fmaf(v_lds[8 * p + 2 * e + 1], __uint_as_float(w[e] & 0xFFFF0000u), s);
+      }
+    };
+#pragma unroll
+    for (int p = 0; p < kTokenSteps; ++p) {
+      if (8 * p >= R) break;
+      add(ahead ? b0[p] : *reinterpret_cast<const v4u*>(b + static_cast<size_t>(n) * R + 8 * p), p);
+    }
+    store_y<BF16>(a.out, row + n, (ahead ? y0 : load_y<BF16>(a.y, row + n)) + s);
+  }
+}
+
 template <int WT, int RS>
 hipError_t launch_expand(const LoraArgs& a, bool bf16, unsigned grid, hipStream_t stream) {
   const dim3 g(grid), b(64 * kExpandWaves);
@@ -509,9 +644,9 @@ hipError_t launch_expand(const LoraArgs& a, bool bf16, unsigned grid, hipStream_
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 // Tokens up to which every pass of a tile of 16 has a workgroup of its own: each
-// token may have its own adapter.  200 tokens of 32 adapters in any order, rank 16,
-// 5120 -> 5120: 22 us, and 42 with four workgroups a tile of 64; the same as four
-// requests of rank 64: 13.5 and 16 us.
+// token may have its own adapter.  200 tokens of 8 adapters in any order, rank 64,
+// 5120 -> 17408: 42 us, and 45 with four workgroups a tile of 64; of four requests,
+// 5120 -> 5120: 13.5 and 16 us.
 constexpr int kSplitPassesM = 256;
 
 // Workgroups that share a tile's passes (pass p, p + passes, ...).  Larger batches
@@ -544,6 +679,17 @@ void plan_shrink(LoraArgs& a, const DeviceInfo& dev) {
   a.slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((want + busy - 1) / busy, a.K / 64 / shrink_waves(a.shrink_ts))));
 }
 
+// Whether lora_token_kernel runs, which needs no workspace: every token has a
+// workgroup and A is a few steps of loads.  Measured on either side, one token and 24
+// of 32 adapters, two kernels in brackets: rank 24, 5120 -> 5120, 7.9 (8.1) and 9.3
+// (10.1) us; rank 8, 17408 -> 5120, three rounds, 7.4 (9.4) and 8.3 (11.1); but rank
+// 32, 5120 -> 17408, 14.4 (13.1) for 24; rank 16, 17408 -> 5120, 10.7 (9.5) and 12.7
+// (11.7).  200 tokens of rank 16, 5120 -> 5120: 13.5 (20.3).
+bool one_launch(const LoraArgs& a, const DeviceInfo& dev) {
+  return a.n > 0 && a.M <= std::min(kSplitPassesM, std::max(1, dev.cu_count)) &&
+         a.R / 8 * ceil_div(a.K, 8 * kTokenThreads) <= kTokenSteps;
+}
+
 template <int TS>
 hipError_t launch_shrink(const LoraArgs& a, unsigned grid, hipStream_t stream) {
   const dim3 g(grid), b(64 * shrink_waves(TS));
@@ -564,6 +710,7 @@ size_t lora_workspace_bytes(int64_t M, int K, int R, int64_t n, const DeviceInfo
   a.K = K;
   a.R = R;
   a.n = static_cast<int>(n);
+  if (one_launch(a, dev)) return 0;
   plan_shrink(a, dev);
   return static_cast<size_t>(a.slices) * static_cast<size_t>(M) * R * sizeof(float);
 }
@@ -571,6 +718,14 @@ size_t lora_workspace_bytes(int64_t M, int K, int R, int64_t n, const DeviceInfo
 hipError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo& dev, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const int cus = std::max(1, dev.cu_count);
+  if (one_launch(a, dev)) {
+    // a round of workgroups, of 256 n at least
+    a.expand_chunks = static_cast<uint32_t>(std::min<int64_t>(cus / a.M, ceil_div(a.N, 256)));
+    const dim3 g(static_cast<unsigned>(a.M * a.expand_chunks)), b(kTokenThreads);
+    if (bf16) hipLaunchKernelGGL(lora_token_kernel<true>, g, b, 0, stream, a);
+    else hipLaunchKernelGGL(lora_token_kernel<false>, g, b, 0, stream, a);
+    return hipGetLastError();
+  }
   plan_shrink(a, dev);
   const int64_t shrink_grid = static_cast<int64_t>(a.shrink_tiles) * a.shrink_passes * a.slices;
   // 64 tokens a workgroup read B once, 16 tokens and 256 n make more workgroups of

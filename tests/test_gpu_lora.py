@@ -193,12 +193,32 @@ def test_python_refusals(twl):
     bad = [dict(y=c["y"].half()), dict(x=c["x"].float()), dict(x=c["x"][:3]), dict(ids=c["ids"].long()), dict(ids=c["ids"][:3]),
            dict(lora_a=c["lora_a"][0]), dict(lora_b=c["lora_b"][:1]), dict(lora_b=c["lora_b"].transpose(1, 2)),
            dict(scale=c["scale"].double()), dict(out=c["y"].bfloat16()), dict(out=c["y"][:2]), dict(out=c["y"].cpu()),
-           dict(lora_a=c["lora_a"][:, :12].contiguous(), lora_b=c["lora_b"][..., :12].contiguous()),
-           dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
-           dict(workspace=c["y"].view(torch.uint8).view(-1))]
+           dict(lora_a=c["lora_a"][:, :12].contiguous(), lora_b=c["lora_b"][..., :12].contiguous())]
     for kw in bad:
         with pytest.raises((ValueError, TypeError, twl.TwlError)):
             twl.lora_add(**{**c, **kw})
     with pytest.raises(twl.TwlError):  # K not a multiple of 128
         twl.lora_add(**{**c, "x": c["x"][:, :120].contiguous(), "lora_a": c["lora_a"][..., :120].contiguous()})
     assert twl.lora_add(**{**c, "y": c["y"][:0], "x": c["x"][:0], "ids": c["ids"][:0]}).shape == (0, 64)
+    c = _case(3, 300, 64, 256, 16, 2, F32, runs)  # two kernels: needs a workspace
+    assert twl.lora_workspace_bytes(300, 256, 16, 2) > 0
+    for ws in (torch.empty(16, dtype=torch.uint8, device="cuda"), c["y"].view(torch.uint8).view(-1)):
+        with pytest.raises((ValueError, twl.TwlError)):
+            twl.lora_add(workspace=ws, **c)
+
+
+@pytest.mark.parametrize("M,N,K,R", [(1, 5120, 5120, 16), (3, 260, 17408, 8), (256, 1000, 768, 24), (200, 2048, 8192, 24),
+                                     (24, 17408, 5120, 16), (20, 77, 8320, 8), (1, 1, 128, 8), (1, 70000, 640, 16)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_launch(twl, M, N, K, R, dtype):
+    """Small adapters of up to 256 tokens take one kernel, without a workspace: shares
+    of n of more than 1024, rows of A of more than 8192, a last round of few threads;
+    in front of a larger buffer, and in place."""
+    assert twl.lora_workspace_bytes(M, K, R, 7) == 0
+    c = _case(M + N, M, N, K, R, 7, dtype, mixed)
+    announce(f"lora one launch M={M} N={N} K={K} R={R} {dtype}")
+    buf = torch.full((M + 1, N), 7.0, dtype=dtype, device="cuda")
+    _check(twl.lora_add(out=buf[:M], **c), c)
+    assert torch.all(buf[M:] == 7.0).item()
+    y = c["y"].clone()
+    _check(twl.lora_add(**dict(c, out=c["y"])), c, y=y)

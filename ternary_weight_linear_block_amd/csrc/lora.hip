@@ -220,22 +220,38 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, size_
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), kRawBufferWord3);
 }
 
-// One wave's 16 tokens x 64 n of y, in y's type, where rows are 16-byte aligned: 8
-// (fp32: 16) lanes a token, 16 bytes each.
-template <bool BF16>
+// One wave's 16 tokens x 64 n of y, in y's type: pieces of 16 bytes, 8 (fp32: 16)
+// lanes a token, where rows are 4-byte aligned (the memory instructions ask for no
+// more); bf16 rows of odd N in pieces of one n, for which 1855 tokens of 9216 -> 5955,
+// rank 64, take 41 us, with 5954 n 37 and 5952 (16-byte aligned) 34.
+template <bool BF16, int PIECE>
 struct Out {
-  static constexpr int kItems = BF16 ? 2 : 4;  // instructions
-  static constexpr int kEach = BF16 ? 8 : 4;   // elements of 16 bytes
-  static constexpr int kLanes = 64 / kEach;    // lanes a token
-  v4u raw[kItems];
+  static constexpr int kSize = BF16 ? 2 : 4;
+  static constexpr int kItems = 16 * kSize / PIECE;  // instructions
+  static constexpr int kEach = PIECE / kSize;        // elements of a piece
+  static constexpr int kLanes = 64 / kEach;          // lanes a token
+  static_assert(PIECE == 16 || (BF16 && PIECE == 2), "pieces");
+  typedef typename std::conditional<PIECE == 16, v4u, uint16_t>::type Raw;
+  Raw raw[kItems];
 
   static __device__ __forceinline__ int token(int i, int lane) { return (64 * i + lane) / kLanes; }
   static __device__ __forceinline__ int column(int lane) { return kEach * (lane % kLanes); }
 
+  static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t buf, uint32_t at) {
+    if constexpr (PIECE == 16) return __builtin_amdgcn_raw_buffer_load_b128(buf, at, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b16(buf, at, 0, 0);
+  }
+  static __device__ __forceinline__ void store(Raw v, __amdgpu_buffer_rsrc_t buf, uint32_t at) {
+    if constexpr (PIECE == 16) __builtin_amdgcn_raw_buffer_store_b128(v, buf, at, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(v, buf, at, 0, 0);
+  }
+
   // adds d[0 ..] to item i
-  __device__ __forceinline__ v4u sum(int i, const float* d) const {
-    v4u w;
-    if constexpr (BF16) {
+  __device__ __forceinline__ Raw sum(int i, const float* d) const {
+    Raw w;
+    if constexpr (PIECE == 2) {
+      w = static_cast<uint16_t>(pack_bf16(__uint_as_float(static_cast<uint32_t>(raw[i]) << 16) + d[0], 0.0f));
+    } else if constexpr (BF16) {
       const v4f lo = *reinterpret_cast<const v4f*>(d), hi = *reinterpret_cast<const v4f*>(d + 4);
       const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
@@ -250,24 +266,23 @@ struct Out {
   }
 };
 
-// The same for rows of any alignment: out = y + d (d in LDS, a row of kStride floats
-// a token; null: nothing) of the tokens of `tokens`, one token an instruction, lane =
-// one n.
+// The same element by element, for the last columns of rows that are no whole number
+// of pieces: out = y + d (d in LDS, a row of kStride floats a token; null: nothing) of
+// the tokens of `tokens`, one token an instruction, lane = one n.  at: byte offset of
+// the first token's element of this lane; row: bytes of a row.
 template <bool BF16, int kStride>
-__device__ __forceinline__ void finish_unaligned(const void* y, void* out, const float* d, uint64_t tokens, size_t row0,
-                                                 int N, int nb, int lane) {
-  if (nb + lane >= N) return;
-  const size_t at0 = row0 * N + nb + lane;
-#pragma unroll 4
+__device__ __forceinline__ void finish_columns(__amdgpu_buffer_rsrc_t y, __amdgpu_buffer_rsrc_t out, const float* d,
+                                               uint32_t tokens, uint32_t at, uint32_t row, bool in, int lane) {
+#pragma unroll 1
   for (int t = 0; t < 16; ++t) {
-    if (((tokens >> t) & 1) == 0) continue;
-    const size_t at = at0 + static_cast<size_t>(t) * N;
+    const uint32_t o = in && ((tokens >> t) & 1) != 0 ? at + t * row : kOutside;
     const float add = d != nullptr ? d[t * kStride + lane] : -0.0f;
     if constexpr (BF16) {
-      const float v = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(y)[at]) << 16);
-      static_cast<uint16_t*>(out)[at] = static_cast<uint16_t>(pack_bf16(v + add, 0.0f));
+      const float v = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b16(y, o, 0, 0)) << 16);
+      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(pack_bf16(v + add, 0.0f)), out, o, 0, 0);
     } else {
-      static_cast<float*>(out)[at] = static_cast<const float*>(y)[at] + add;
+      const float v = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(y, o, 0, 0));
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v + add), out, o, 0, 0);
     }
   }
 }
@@ -305,9 +320,9 @@ struct ExpandLds {
         vd(std::max((bf16 ? 2 : 3) * 16 * wt * row * 2, kExpandWaves * 16 * kOutStride * 4)) {}
 };
 
-template <int WT, int RS, bool BF16, bool VEC>
+template <int WT, int RS, bool BF16, int PIECE>
 __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs a) {
-  using Y = Out<BF16>;
+  using Y = Out<BF16, PIECE>;
   constexpr ExpandLds L(WT, RS, BF16);
   constexpr int TM = 16 * WT, WN = kExpandWaves / WT, TERMS = BF16 ? 2 : 3;
   constexpr int kStride = L.row, NB = L.bufs;
@@ -347,29 +362,31 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
     const int t = 16 * wt + Y::token(i, lane);
     return ((tokens >> t) & 1) != 0 ? static_cast<uint32_t>(t * N + col) * kSize : kOutside;
   };
-  const auto at = [&](uint32_t piece0, int nb) { return nb + col < n_hi ? piece0 + static_cast<uint32_t>(nb) * kSize : kOutside; };
-  const size_t row0 = static_cast<size_t>(t0 + 16 * wt);
+  // ranges below n_vec are whole pieces, the row's last may go element by element
+  const int n_vec = N % Y::kEach == 0 ? n_hi : min(n_hi, N & ~63);
+  const auto at = [&](uint32_t piece0, int nb) { return nb + col < n_vec ? piece0 + static_cast<uint32_t>(nb) * kSize : kOutside; };
+  const auto finish = [&](const float* d, uint64_t tokens, int nb) {
+    finish_columns<BF16, kOutStride>(y_buf, out_buf, d, static_cast<uint32_t>(tokens >> (16 * wt)),
+                                     static_cast<uint32_t>(16 * wt * N + nb + lane) * kSize, static_cast<uint32_t>(N) * kSize,
+                                     nb + lane < N, lane);
+  };
 
   // tokens without an adapter: copied with the tile's first pass, or here if it has none
   uint64_t none = a.out != a.y && p == 0 ? __ballot(passes.id < 0 && lane < TM && t0 + lane < a.M) : 0;
   if (passes.rest == 0) {
     for (int nb = n_lo; nb < n_hi; nb += 4 * step) {
-      if constexpr (VEC) {
-        v4u y[4][Y::kItems];
+      typename Y::Raw y[4][Y::kItems];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int i = 0; i < Y::kItems; ++i)
-            y[u][i] = __builtin_amdgcn_raw_buffer_load_b128(y_buf, at(piece(none, i), nb + u * step), 0, 0);
+        for (int i = 0; i < Y::kItems; ++i) y[u][i] = Y::load(y_buf, at(piece(none, i), nb + u * step));
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int i = 0; i < Y::kItems; ++i)
-            __builtin_amdgcn_raw_buffer_store_b128(y[u][i], out_buf, at(piece(none, i), nb + u * step), 0, 0);
-      } else {
-        for (int u = 0; u < 4 && nb + u * step < n_hi; ++u)
-          finish_unaligned<BF16, kOutStride>(a.y, a.out, nullptr, none >> (16 * wt), row0, N, nb + u * step, lane);
-      }
+        for (int i = 0; i < Y::kItems; ++i) Y::store(y[u][i], out_buf, at(piece(none, i), nb + u * step));
+      for (int u = 0; u < 4; ++u)
+        if (nb + u * step >= n_vec && nb + u * step < n_hi)
+          finish(nullptr, none, nb + u * step);
     }
     return;
   }
@@ -410,14 +427,12 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
     for (int i = 0; i < Y::kItems; ++i) own[i] = piece(written, i);
     const auto load_y = [&](Y& y, int nb) {
 #pragma unroll
-      for (int i = 0; i < Y::kItems; ++i) y.raw[i] = __builtin_amdgcn_raw_buffer_load_b128(y_buf, at(own[i], nb), 0, 0);
+      for (int i = 0; i < Y::kItems; ++i) y.raw[i] = Y::load(y_buf, at(own[i], nb));
     };
     Y even, odd;
     load_b(n_lo);
-    if (VEC) {
-      load_y(even, n_lo);
-      load_y(odd, n_lo + step);
-    }
+    load_y(even, n_lo);
+    load_y(odd, n_lo + step);
     const float scale = a.scale[adapter];
     lds_barrier();  // the previous pass's products have been read
     for (int e = threadIdx.x; e < TM * 8 * RS; e += 64 * kExpandWaves) {
@@ -479,19 +494,19 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
         *reinterpret_cast<v4f*>(dw + j * kOutStride + 16 * f + 4 * q) = acc[f];
       }
       wave_lds_sync();
-      if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < Y::kItems; ++i)
-          __builtin_amdgcn_raw_buffer_store_b128(y.sum(i, dw + Y::token(i, lane) * kOutStride + col), out_buf, at(own[i], nb), 0, 0);
-        load_y(y, nb + 2 * step);
-      } else {
-        finish_unaligned<BF16, kOutStride>(a.y, a.out, dw, written >> (16 * wt), row0, N, nb, lane);
-      }
+      for (int i = 0; i < Y::kItems; ++i)
+        Y::store(y.sum(i, dw + Y::token(i, lane) * kOutStride + col), out_buf, at(own[i], nb));
+      load_y(y, nb + 2 * step);
     };
     for (int nb = n_lo; nb < n_end; nb += 2 * step) {
       range(even, nb, 0);
       if (nb + step < n_end) range(odd, nb + step, 1);
     }
+    // the products of the wave's last range are still there
+    const int nb = n_lo + (n_end - n_lo - 1) / step * step;
+    if (n_end > n_lo && nb >= n_vec && nb < n_hi)
+      finish(dw, written, nb);
   }
 }
 
@@ -633,11 +648,9 @@ __global__ __launch_bounds__(kTokenThreads) void lora_token_kernel(LoraArgs a) {
 template <int WT, int RS>
 hipError_t launch_expand(const LoraArgs& a, bool bf16, unsigned grid, hipStream_t stream) {
   const dim3 g(grid), b(64 * kExpandWaves);
-  const bool vec = a.N % (bf16 ? 8 : 4) == 0;  // rows of y 16-byte aligned
-  if (bf16 && vec) hipLaunchKernelGGL((lora_expand_kernel<WT, RS, true, true>), g, b, 0, stream, a);
-  else if (bf16) hipLaunchKernelGGL((lora_expand_kernel<WT, RS, true, false>), g, b, 0, stream, a);
-  else if (vec) hipLaunchKernelGGL((lora_expand_kernel<WT, RS, false, true>), g, b, 0, stream, a);
-  else hipLaunchKernelGGL((lora_expand_kernel<WT, RS, false, false>), g, b, 0, stream, a);
+  if (!bf16) hipLaunchKernelGGL((lora_expand_kernel<WT, RS, false, 16>), g, b, 0, stream, a);
+  else if (a.N % 2 == 0) hipLaunchKernelGGL((lora_expand_kernel<WT, RS, true, 16>), g, b, 0, stream, a);
+  else hipLaunchKernelGGL((lora_expand_kernel<WT, RS, true, 2>), g, b, 0, stream, a);
   return hipGetLastError();
 }
 

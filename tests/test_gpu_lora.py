@@ -91,6 +91,13 @@ BF, F32 = torch.bfloat16, torch.float32
     (1040, 77, 256, 8, 3, runs),
     (1100, 136, 256, 32, 40, mixed),
     (1025, 16392, 128, 24, 6, runs),
+    # rows that are no whole pieces of 16 bytes: 4-byte aligned, odd, shorter than one range
+    (300, 1002, 512, 64, 5, runs),
+    (400, 10713, 128, 32, 3, runs),
+    (270, 66, 512, 128, 4, mixed),
+    (1100, 63, 256, 16, 6, runs),
+    (4200, 4099, 128, 16, 3, runs),
+    (90, 4666, 2048, 32, 9, mixed),
 ])
 def test_values(twl, M, N, K, R, n, ids, dtype):
     announce(f"lora M={M} N={N} K={K} R={R} n={n} {dtype}")
@@ -98,7 +105,7 @@ def test_values(twl, M, N, K, R, n, ids, dtype):
     _check(twl.lora_add(**c), c)
 
 
-@pytest.mark.parametrize("M,N", [(5, 136), (70, 136), (260, 16384)])
+@pytest.mark.parametrize("M,N", [(5, 136), (70, 136), (260, 16384), (300, 1003), (290, 70), (333, 16386), (270, 3)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_in_place_and_no_adapter(twl, M, N, dtype):
     """y updated in place; every token without an adapter, also by ids out of range."""

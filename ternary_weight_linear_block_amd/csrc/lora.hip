@@ -522,8 +522,8 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
 // tokens of 32 adapters on 5120 x 17408 (12.0): ids, A, the sums and B in turn, and
 // 1 us at least for each eight rows.
 constexpr int kTokenThreads = 1024;
-constexpr int kTokenSteps = 3;             // of eight rows of 8192 k
-constexpr int kTokenR = 8 * kTokenSteps;   // largest rank
+constexpr int kTokenR = 24;     // largest rank
+constexpr int kTokenSteps = 4;  // of eight rows of 8192 k
 
 // lanes exchanged by a DPP control: 0x128 l ^ 8, 0x141 l ^ 7, 0x4E l ^ 2, 0xB1 l ^ 1
 template <int CTRL>
@@ -596,9 +596,9 @@ __global__ __launch_bounds__(kTokenThreads) void lora_token_kernel(LoraArgs a) {
   };
   Step cur, next;
   load(cur, 0, 0);
-  v4u b0[kTokenSteps];  // the first n's row of B
+  v4u b0[kTokenR / 8];  // the first n's row of B
 #pragma unroll
-  for (int p = 0; p < kTokenSteps; ++p) b0[p] = *reinterpret_cast<const v4u*>(b + static_cast<size_t>(n0) * R + 8 * min(p, R / 8 - 1));
+  for (int p = 0; p < kTokenR / 8; ++p) b0[p] = *reinterpret_cast<const v4u*>(b + static_cast<size_t>(n0) * R + 8 * min(p, R / 8 - 1));
   float acc[8] = {};
   int r0 = 0, round = 0;
   const int steps = (R / 8) * rounds;
@@ -646,7 +646,7 @@ __global__ __launch_bounds__(kTokenThreads) void lora_token_kernel(LoraArgs a) {
       }
     };
 #pragma unroll
-    for (int p = 0; p < kTokenSteps; ++p) {
+    for (int p = 0; p < kTokenR / 8; ++p) {
       if (8 * p >= R) break;
       add(ahead ? b0[p] : *reinterpret_cast<const v4u*>(b + static_cast<size_t>(n) * R + 8 * p), p);
     }
@@ -702,14 +702,15 @@ void plan_shrink(LoraArgs& a, const DeviceInfo& dev) {
 }
 
 // Whether lora_token_kernel runs, which needs no workspace: every token has a
-// workgroup and A is a few steps of loads.  Measured on either side, one token and 24
-// of 32 adapters, two kernels in brackets: rank 24, 5120 -> 5120, 7.9 (8.1) and 9.3
-// (10.1) us; rank 8, 17408 -> 5120, three rounds, 7.4 (9.4) and 8.3 (11.1); but rank
-// 32, 5120 -> 17408, 14.4 (13.1) for 24; rank 16, 17408 -> 5120, 10.7 (9.5) and 12.7
-// (11.7).  200 tokens of rank 16, 5120 -> 5120: 13.5 (20.3).
+// workgroup and A is a few steps of loads.  Measured on either side, one token (M = 6
+// for 10240) and 24 of 32 adapters, two kernels in brackets: rank 24, 5120 -> 5120, 7.4
+// (8.1) and 8.6 (10.1) us; rank 16, 10240 -> 2000, two rounds, 8.5 (8.8) and 8.9
+// (10.2); but rank 32, 5120 -> 5120, 8.8 (7.9) and 10.9 (10.4); rank 16, 17408 ->
+// 5120, three rounds, 10.7 (9.5) and 12.7 (11.7).  200 tokens of rank 16, 5120 ->
+// 5120: 13.2 (20.3).
 bool one_launch(const LoraArgs& a, const DeviceInfo& dev) {
   return a.n > 0 && a.M <= std::min(kSplitPassesM, std::max(1, dev.cu_count)) &&
-         a.R / 8 * ceil_div(a.K, 8 * kTokenThreads) <= kTokenSteps;
+         a.R <= kTokenR && a.R / 8 * ceil_div(a.K, 8 * kTokenThreads) <= kTokenSteps;
 }
 
 template <int TS>

@@ -215,7 +215,7 @@ def test_python_refusals(twl):
 
 
 @pytest.mark.parametrize("M,N,K,R", [(1, 5120, 5120, 16), (3, 260, 17408, 8), (256, 1000, 768, 24), (200, 2048, 8192, 24),
-                                     (24, 17408, 5120, 16), (20, 77, 8320, 8), (1, 1, 128, 8), (1, 70000, 640, 16)])
+                                     (24, 17408, 5120, 16), (20, 77, 8320, 8), (40, 130, 16384, 16), (1, 1, 128, 8), (1, 70000, 640, 16)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_one_launch(twl, M, N, K, R, dtype):
     """Small adapters of up to 256 tokens take one kernel, without a workspace: shares

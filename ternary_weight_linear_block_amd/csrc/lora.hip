@@ -276,13 +276,15 @@ __device__ __forceinline__ void finish_columns(__amdgpu_buffer_rsrc_t y, __amdgp
 #pragma unroll 1
   for (int t = 0; t < 16; ++t) {
     const uint32_t o = in && ((tokens >> t) & 1) != 0 ? at + t * row : kOutside;
-    const float add = d != nullptr ? d[t * kStride + lane] : -0.0f;
     if constexpr (BF16) {
-      const float v = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b16(y, o, 0, 0)) << 16);
-      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(pack_bf16(v + add, 0.0f)), out, o, 0, 0);
+      uint16_t v = __builtin_amdgcn_raw_buffer_load_b16(y, o, 0, 0);
+      if (d != nullptr)
+        v = static_cast<uint16_t>(pack_bf16(__uint_as_float(static_cast<uint32_t>(v) << 16) + d[t * kStride + lane], 0.0f));
+      __builtin_amdgcn_raw_buffer_store_b16(v, out, o, 0, 0);
     } else {
-      const float v = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(y, o, 0, 0));
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v + add), out, o, 0, 0);
+      uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(y, o, 0, 0);
+      if (d != nullptr) v = __float_as_uint(__uint_as_float(v) + d[t * kStride + lane]);
+      __builtin_amdgcn_raw_buffer_store_b32(v, out, o, 0, 0);
     }
   }
 }
@@ -420,11 +422,13 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
       }
     };
     const uint64_t written = tokens | none;
-    const bool copied = ((none >> (16 * wt + j)) & 1) != 0;  // token j takes nothing from this adapter
-    none = 0;
     uint32_t own[Y::kItems];
+    bool copied[Y::kItems];  // this token takes nothing from the adapter
 #pragma unroll
-    for (int i = 0; i < Y::kItems; ++i) own[i] = piece(written, i);
+    for (int i = 0; i < Y::kItems; ++i) {
+      own[i] = piece(written, i);
+      copied[i] = ((none >> (16 * wt + Y::token(i, lane))) & 1) != 0;
+    }
     const auto load_y = [&](Y& y, int nb) {
 #pragma unroll
       for (int i = 0; i < Y::kItems; ++i) y.raw[i] = Y::load(y_buf, at(own[i], nb));
@@ -489,14 +493,13 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
       // lane (j, q) holds n = nb + 16 f + 4 q .. + 3 of token j
       wave_lds_sync();  // the previous products have been read
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        if (copied) acc[f] = v4f{-0.0f, -0.0f, -0.0f, -0.0f};  // y + -0 is y
-        *reinterpret_cast<v4f*>(dw + j * kOutStride + 16 * f + 4 * q) = acc[f];
-      }
+      for (int f = 0; f < 4; ++f) *reinterpret_cast<v4f*>(dw + j * kOutStride + 16 * f + 4 * q) = acc[f];
       wave_lds_sync();
 #pragma unroll
-      for (int i = 0; i < Y::kItems; ++i)
-        Y::store(y.sum(i, dw + Y::token(i, lane) * kOutStride + col), out_buf, at(own[i], nb));
+      for (int i = 0; i < Y::kItems; ++i) {
+        const typename Y::Raw sum = y.sum(i, dw + Y::token(i, lane) * kOutStride + col);
+        Y::store(copied[i] ? y.raw[i] : sum, out_buf, at(own[i], nb));
+      }
       load_y(y, nb + 2 * step);
     };
     for (int nb = n_lo; nb < n_end; nb += 2 * step) {
@@ -505,8 +508,11 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
     }
     // the products of the wave's last range are still there
     const int nb = n_lo + (n_end - n_lo - 1) / step * step;
-    if (n_end > n_lo && nb >= n_vec && nb < n_hi)
-      finish(dw, written, nb);
+    if (n_end > n_lo && nb >= n_vec && nb < n_hi) {
+      finish(dw, tokens, nb);
+      finish(nullptr, none, nb);
+    }
+    none = 0;
   }
 }
 
@@ -514,11 +520,11 @@ __global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs
 //
 // A workgroup computes all of its token's v: thread = 8 k of every row of A, eight
 // rows in flight and the next eight behind them, fp32 sums by v_dot2_f32_bf16, lanes
-// by rotations, waves in LDS in order.  Then thread = one n: R products with v in
+// by exchanges, waves in LDS in order.  Then thread = one n: R products with v in
 // fp32.  Every workgroup of a token reads its A again (from L2), which costs less
 // than a second launch and its latencies as long as A is small.
 //
-// 6.8 us for one token of rank 16 on 5120 x 5120 (two kernels: 8.0), 9.3 us for 24
+// 6.2 us for one token of rank 16 on 5120 x 5120 (two kernels: 8.0), 9.1 us for 24
 // tokens of 32 adapters on 5120 x 17408 (12.0): ids, A, the sums and B in turn, and
 // 1 us at least for each eight rows.
 constexpr int kTokenThreads = 1024;
@@ -574,7 +580,9 @@ __global__ __launch_bounds__(kTokenThreads) void lora_token_kernel(LoraArgs a) {
   const int id = __builtin_amdgcn_readfirstlane(a.ids[t]);
   if (id < 0 || id >= a.n) {
     if (a.out == a.y) return;
-    for (int n = n_lo + tid; n < n_hi; n += kTokenThreads) store_y<BF16>(a.out, row + n, load_y<BF16>(a.y, row + n));
+    typedef typename std::conditional<BF16, uint16_t, uint32_t>::type Bits;
+    for (int n = n_lo + tid; n < n_hi; n += kTokenThreads)
+      static_cast<Bits*>(a.out)[row + n] = static_cast<const Bits*>(a.y)[row + n];
     return;
   }
   const uint16_t* b = a.b + static_cast<size_t>(id) * N * R;

@@ -195,6 +195,24 @@ def test_two_streams_and_graphs(twl):
             _check(o, c)
 
 
+@pytest.mark.parametrize("M,R", [(9, 16), (9, 64), (300, 32)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tokens_without_adapter_keep_their_bits(twl, M, R, dtype):
+    """NaN with any payload, infinities, denormals and minus zero are copied."""
+    N = 90
+    c = _case(M, M, N, 256, R, 3, dtype, [(-1, 1, 7)[t % 3] for t in range(M)])
+    if dtype == BF:
+        bits = torch.tensor([0x7F81, -0x0001, 0x7F80, -0x0080, 0x0001, -0x8000], dtype=torch.int16, device="cuda")
+    else:
+        bits = torch.tensor([0x7F800001, -1, 0x7F800000, -0x00800000, 1, -0x80000000], dtype=torch.int32, device="cuda")
+    c["y"] = bits.repeat(M * N // 6 + 1)[:M * N].view(M, N).view(dtype)
+    announce(f"lora bits M={M} R={R} {dtype}")
+    out = twl.lora_add(**c)
+    rows = [t for t in range(M) if t % 3 != 1]
+    kind = torch.int16 if dtype == BF else torch.int32
+    assert torch.equal(out.view(kind)[rows], c["y"].view(kind)[rows])
+
+
 def test_python_refusals(twl):
     c = _case(3, 4, 64, 256, 16, 2, F32, [0, 1, 0, 1])
     bad = [dict(y=c["y"].half()), dict(x=c["x"].float()), dict(x=c["x"][:3]), dict(ids=c["ids"].long()), dict(ids=c["ids"][:3]),

@@ -372,7 +372,8 @@ twl_status twl_lora_add(const void* y, const uint16_t* x, const int32_t* ids, co
                         int64_t R, int64_t n_adapters, int kind, void* out, void* workspace,
                         size_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace twl_lora_add needs on the current device (0 for invalid sizes). */
+/* Bytes of workspace twl_lora_add needs on the current device (0 where it needs none,
+ * and for invalid sizes). */
 size_t twl_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t n_adapters);
 
 /*

@@ -352,25 +352,27 @@ void norm_rotate_kernel(NormArgs a) {
       }
       const rot::TokenQuant tq = rot::token_quant_unscaled(tmax);
       if (threadIdx.x == 0) a.a_scale[t] = tq.scale;
-      const auto store_all = [&](auto quotient) {
+      // run c of a lane's four runs of 4 consecutive elements, as one dword
+      const auto store_all = [&](auto run) {
 #pragma unroll
         for (int i = 0; i < BPW; ++i) {
           const int b = wave + i * nw;
           if (b >= nblocks) continue;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t word = 0;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) word |= rot::quant_byte(quotient(r[i][4 * c + d])) << (8 * d);
-            *reinterpret_cast<uint32_t*>(a.x_i8 + row + b * kBlock + 256 * c + 4 * lane) = word;
-          }
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint32_t*>(a.x_i8 + row + b * kBlock + 256 * c + 4 * lane) = run(&r[i][4 * c]);
         }
       };
       // the test is hoisted out of the element loop (one branch per token)
       if (tq.markstein)
-        store_all([&](float w) { return rot::quotient_markstein(w, tq); });
+        store_all([&](const float* w) { return rot::quant_run_markstein(w, tq); });
       else
-        store_all([&](float w) { return rot::quotient_unscaled(w, tq); });
+        store_all([&](const float* w) {
+          uint32_t word = 0;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) word |= rot::quant_byte(rot::quotient_unscaled(w[d], tq)) << (8 * d);
+          return word;
+        });
     }
   }
 }

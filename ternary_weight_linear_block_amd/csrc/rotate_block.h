@@ -271,6 +271,17 @@ __device__ __forceinline__ float quotient_markstein(float w, const TokenQuant& t
   return __builtin_fmaf(__builtin_fmaf(-q0, t.div, w), t.inv, q0);
 }
 
+// Four consecutive elements as one dword where markstein holds.  No quotient passes
+// 127 by more than a rounding there, so nothing is clamped, and adding 1.5 * 2^23
+// rounds to nearest even with the integer's low byte in place (2.5 instructions an
+// element less than rint, clamp, conversion and shift).
+__device__ __forceinline__ uint32_t quant_run_markstein(const float* w, const TokenQuant& t) {
+  uint32_t u[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) u[d] = __float_as_uint(quotient_markstein(w[d], t) + 12582912.0f);
+  return __builtin_amdgcn_perm(u[1], u[0], 0x0C0C0400u) | __builtin_amdgcn_perm(u[3], u[2], 0x04000C0Cu);
+}
+
 // Layout-2 run c of a lane (elements 256 c + 4 lane .. + 3) as one dword of
 // four int8 values, low element first.
 __device__ __forceinline__ uint32_t quant_run(const float (&w)[16], int c, const TokenQuant& t) {

@@ -22,11 +22,11 @@
 // Workgroups stay and take every gridDim.x-th token; with one block a wave the
 // next token's rows are loaded while this one is computed.
 //
-// 8192 tokens of 5120 with everything: 119 us, 3.9 TB/s of the 461 MB that have to
-// move (a copy reaches 5.15): the fp64 and rotation instructions, 2500 cycles a
+// 8192 tokens of 5120 with everything: 116 us, 4.0 TB/s of the 461 MB that have to
+// move (a copy reaches 5.15): the fp64 and rotation instructions, 2300 cycles a
 // block, take as long as the memory and overlap it in part.  333 tokens of 17408,
-// the norm alone: 13.4 us, the instructions of the CUs that have two tokens.  One
-// token of 5120: 5.7 us, two rounds of loads, three barriers and the rotation in
+// the norm alone: 12.8 us, the instructions of the CUs that have two tokens.  One
+// token of 5120: 5.5 us, two rounds of loads, three barriers and the rotation in
 // turn.
 #include "rotate_block.h"
 

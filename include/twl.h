@@ -331,8 +331,9 @@ int twl_rotate_quant_linear_fused(int64_t M, int64_t N, int64_t K);
  *   x_i8        out: int8 [M, K];  a_scale out: fp32 [M]  (NULL when sign is)
  * eps must be positive.  Outputs that overlap an input (other than h) or each
  * other are TWL_EINVAL.  A row whose values are not finite gives unspecified
- * results in that row only.  A product x * post_weight * gate or h * weight below
- * 2^-126 is rounded to a multiple of 2^-149 before the norm's factor.
+ * results in that row only, and so do normed values of 2^116 or more (a row's
+ * element times its norm's factor and weight); one below 2^-118 may be off by
+ * 2^-142 before the gate.  bf16() rounds to fp32 first.
  */
 twl_status twl_norm_rotate_quant_act(const uint16_t* x, const uint16_t* residual,
                                      const uint16_t* post_weight, const uint16_t* gate,

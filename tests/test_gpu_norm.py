@@ -233,3 +233,45 @@ def test_python_refusals(twl):
         f(x, w, None)
     out = f(x[:0], w, sign)
     assert out[0].shape == (0, 1024)
+
+
+# exponents of x, post_weight, gate, branch_scale, residual and weight (None: not
+# there); products of some of them leave fp32's range on either side, h and n do not
+@pytest.mark.parametrize("x,post,gate,scale,residual,weight", [
+    (100, None, 40, -60, None, 0),     # x * gate above 2^128
+    (100, None, 40, -60, 79, 0),
+    (60, 100, 60, -120, None, 0),      # x * post_weight, and times gate
+    (120, 100, 20, -90, 29, 0),        # the same of a row whose squares pass fp32's range
+    (-100, None, -60, 150, None, 0),   # x * gate below 2^-149
+    (-60, -70, -60, 130, 0, 0),
+    (60, None, None, 0, 60, 100),      # h * weight above 2^128
+    (-60, None, None, 0, -60, -110),   # and below 2^-149: n is 2^-110
+    (11, None, None, 0, 11, 112),      # the largest and smallest rows that are not scaled
+    (-7, None, None, 0, -7, -117),
+])
+@pytest.mark.parametrize("M,K,gate_rows", [(3, 1024, True), (2, 17408, False), (1, 33792, True)])
+def test_products_outside_fp32(twl, M, K, gate_rows, x, post, gate, scale, residual, weight):
+    c = _case(41, M, K, residual is not None, post is not None,
+              "none" if gate is None else "token" if gate_rows else "channel")
+    c["branch_scale"], c["eps"] = 2.0 ** scale, 1e-40
+    for name, e in (("x_bits", x), ("post_bits", post), ("gate_bits", gate), ("residual_bits", residual), ("weight_bits", weight)):
+        if e is not None:
+            c[name] = W.f32_to_bf16_bits((W.bf16_bits_to_f32(c[name]).astype(np.float64) * 2.0 ** e).astype(np.float32))
+    _, oa, oh, on = B.norm_rotate_quant_act(**c)
+    for bits in (oh, on):  # what is defined is finite and not flushed
+        v = W.bf16_bits_to_f32(bits)
+        assert np.isfinite(v).all() and np.abs(v).max() > 2.0 ** -120
+    announce(f"norm products M={M} K={K} x={x} post={post} gate={gate} scale={scale} residual={residual} weight={weight}")
+    _check(_run(twl, c), c)
+
+
+@pytest.mark.parametrize("M,K", [(800, 2048), (3, 2048)])
+@pytest.mark.parametrize("x,weight", [(60, 100), (-60, -80)])
+def test_products_outside_fp32_of_the_norm_alone(twl, M, K, x, weight):
+    """h is x itself; the second of two tokens of a workgroup too."""
+    c = _case(43, M, K, False, False, "none")
+    c["eps"] = 1e-40
+    for name, e in (("x_bits", x), ("weight_bits", weight)):
+        c[name] = W.f32_to_bf16_bits(W.bf16_bits_to_f32(c[name]) * np.float32(2.0 ** e))
+    announce(f"norm alone, products M={M} x={x} weight={weight}")
+    _check(_run(twl, c), c)

@@ -396,7 +396,7 @@ twl_status twl_pack_ternary_gated(const int8_t* code_gate, const uint16_t* s_gat
  *   g = acc[t,2i] a_scale[t] smax[2i] / 127,  u = the same of row 2 i + 1  (fp32,
  *   bit for bit what ternary_linear writes for those rows),
  *   out[t,i] = g / (1 + exp(-g)) * u
- * in fp32 with the native exponential and reciprocal, within (|g| + 6) 2^-24
+ * in fp32 with the native exponential and reciprocal, within (1.25 |g| + 8) 2^-24
  * relative (0 where the logistic of g is below 2^-126), rounded once.  Unlike
  * silu_mul_rotate_quant_act after a bf16 projection, g and u are not rounded and
  * never written.

@@ -49,9 +49,9 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
 }
 
 // SiLU(g) u = g u / (1 + e^-g), by the native exponential and reciprocal (1 ulp
-// each).  The rounding of g log2(e) enters e^-g as |g| 2^-24, so the result is
-// within (|g| + 6) 2^-24 relative: below half a bf16 step by a factor of 2^10 at
-// |g| = 50.  Where 1 + e^-g passes 2^126 (g below -87) the reciprocal is below the
+// each).  The rounding of g log2(e) enters e^-g as |g| 2^-24 and the constant's own
+// error (0.224 2^-24) as 0.224 |g| 2^-24, so the result is within (1.25 |g| + 8) 2^-24
+// relative: below half a bf16 step by a factor of 900 at |g| = 50.  Where 1 + e^-g passes 2^126 (g below -87) the reciprocal is below the
 // smallest normal number and comes out as 0.  Every kernel of ternary_gated_linear uses this
 // form, so all of them give the same bits.
 __device__ __forceinline__ float silu_mul(float g, float u) {

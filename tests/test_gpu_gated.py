@@ -171,3 +171,34 @@ def test_python_refusals(twl):
     with pytest.raises(ValueError):
         twl.pack_ternary_gated(dev(c["gate"].code), s, dev(c["up"].code[:63]), s)
     assert f(x[:0], a[:0], *w).shape == (0, 64)
+
+
+@pytest.mark.parametrize("M,N", [(24, 4), (24, 2048), (4096, 4)])
+def test_silu_bound(twl, M, N):
+    """The bound that twl.h states for the activation, (1.25 |g| + 8) 2^-24, with g
+    and u exact: sums of +-1 and a smax of 127 / 128, whose 127th part is 2^-7, so g
+    and u are a_scale with another exponent.  Dense around -44.38, where the
+    rounding of g log2(e) and the error of its constant add up."""
+    assert np.float32(127 / 128) * (np.float32(1) / np.float32(127)) == np.float32(2.0 ** -7)
+    K = 1024
+    gate = np.zeros((N, K), np.int8)
+    up = np.zeros((N, K), np.int8)
+    gate[0::2, 128], gate[1::2, 128], up[:, 128] = -1, 1, 1
+    s = np.full((N, K // 128), 1 / 128, np.float16)   # q = 1 there
+    s[:, 0] = 127 / 128                              # and 127 in the first group
+    x = np.zeros((M, K), np.int8)
+    x[:, 128] = 1
+    rng = np.random.default_rng(M)
+    g = np.where(rng.random(M) < 0.5, rng.uniform(44.2, 44.6, M), np.exp(rng.uniform(np.log(0.01), np.log(86), M))).astype(np.float32)
+    g[0] = 44.3821
+    w = twl.pack_ternary_gated(dev(gate), dev(s.view(np.int16)), dev(up), dev(s.view(np.int16)))
+    announce(f"silu bound M={M} N={N}")
+    out = host(twl.ternary_gated_linear(dev(x), dev(g * np.float32(128)), *w, out_dtype=torch.float32)).astype(np.float64)
+    u = g.astype(np.float64)
+    for row, sign in ((0, -1.0), (1, 1.0)):
+        want = sign * u / (1.0 + np.exp(-sign * u)) * u
+        err = np.abs(out[:, row] - want) / np.abs(want)
+        over = err - (1.25 * u + 8) * U
+        at = int(np.argmax(over))
+        assert over[at] <= 0, (sign * u[at], err[at] / U)
+        assert np.array_equal(out[:, row], out[:, row + 2])

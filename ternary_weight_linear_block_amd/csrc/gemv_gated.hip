@@ -8,9 +8,10 @@
 //
 // Wide layers run the row-balanced kernel (gemv_rows.h) with whole pairs of rows
 // to a workgroup: both sums of a pair are then in its LDS and the product is
-// formed there, in the same launch.  Layers too narrow for it run the linear
-// layer's dot4 or K-split kernel up to its int32 partial sums and the finishing
-// kernel below, which takes the place of its reduce kernel.
+// formed there, in the same launch.  Layers it does not take (fewer than 16 rows a
+// CU, or K above 33792 at any width) run the linear layer's dot4 or K-split kernel up
+// to its int32 partial sums and the finishing kernel below, which takes the place of
+// its reduce kernel.
 //
 // 2 x 17408 x 5120: 12 us for one token (46 MB, 3.9 TB/s, what the row-balanced
 // kernel reaches for the plain layer of as many rows) and 16.7 us for 24, bound by
@@ -25,25 +26,23 @@ namespace twl {
 namespace {
 
 // Sum of the slices' partial sums of both rows of a pair, then the rescale and
-// the product.  One thread a result.
+// the product.  One thread a result, a row of workgroups a token.
 __global__ __launch_bounds__(256) void gated_finish_kernel(const int32_t* __restrict__ part, int slices, int M, int N,
                                                            const float* __restrict__ a_scale,
                                                            const float* __restrict__ smax,
                                                            void* __restrict__ out, int out_kind) {
-  const int pairs = N / 2;
-  const int total = M * pairs;  // M <= 24 and N < 16 rows a CU: far below 2^31
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
-    const int t = i / pairs, pr = i - t * pairs;
-    int2 s = make_int2(0, 0);
-    for (int sl = 0; sl < slices; ++sl) {
-      const int2 v = *reinterpret_cast<const int2*>(part + (static_cast<size_t>(sl) * M + t) * N + 2 * pr);
-      s.x += v.x;
-      s.y += v.y;
-    }
-    const float g = static_cast<float>(s.x) * a_scale[t] * (smax[2 * pr] * (1.0f / 127.0f));
-    const float u = static_cast<float>(s.y) * a_scale[t] * (smax[2 * pr + 1] * (1.0f / 127.0f));
-    store_out(out, i, out_kind == kOutGatedBf16 ? kOutBf16 : kOutF32, 0, silu_mul(g, u));
+  const int pairs = N / 2, t = blockIdx.y;
+  const int pr = blockIdx.x * 256 + threadIdx.x;  // pairs is at most 2^29
+  if (pr >= pairs) return;
+  int2 s = make_int2(0, 0);
+  for (int sl = 0; sl < slices; ++sl) {
+    const int2 v = *reinterpret_cast<const int2*>(part + (static_cast<size_t>(sl) * M + t) * N + 2 * pr);
+    s.x += v.x;
+    s.y += v.y;
   }
+  const float g = static_cast<float>(s.x) * a_scale[t] * (smax[2 * pr] * (1.0f / 127.0f));
+  const float u = static_cast<float>(s.y) * a_scale[t] * (smax[2 * pr + 1] * (1.0f / 127.0f));
+  store_out(out, static_cast<size_t>(t) * pairs + pr, out_kind == kOutGatedBf16 ? kOutBf16 : kOutF32, 0, silu_mul(g, u));
 }
 
 }  // namespace
@@ -81,8 +80,8 @@ hipError_t launch_gemv_gated(const int8_t* x_i8, const float* a_scale, const uin
   }
   const hipError_t e = launch_gemv_part(x_i8, packed, q, M, N, K, static_cast<int32_t*>(part), dev, stream);
   if (e != hipSuccess) return e;
-  const int blocks = static_cast<int>((M * (N / 2) + 255) / 256);
-  hipLaunchKernelGGL(gated_finish_kernel, dim3(blocks), dim3(256), 0, stream, static_cast<const int32_t*>(part),
+  const dim3 grid(static_cast<unsigned>((N / 2 + 255) / 256), static_cast<unsigned>(M));
+  hipLaunchKernelGGL(gated_finish_kernel, grid, dim3(256), 0, stream, static_cast<const int32_t*>(part),
                      gemv_part_slices(M, N, K, dev), static_cast<int>(M), static_cast<int>(N), a_scale, smax, out,
                      static_cast<int>(out_kind));
   return hipGetLastError();

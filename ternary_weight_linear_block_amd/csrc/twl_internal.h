@@ -90,7 +90,8 @@ size_t gemv_workspace_bytes(int64_t M, int64_t N, int64_t K, GemvKind kind, cons
 // The decode plan for this shape, as twl_plan_info reports it (info[0..7]).
 void gemv_plan_info(int64_t M, int64_t N, int64_t K, GemvKind kind, const DeviceInfo& dev, int64_t* info);
 
-// The decode kernels for narrow layers (the dot4 or K-split MFMA kernel by M) up to
+// The decode kernels for layers that the row-balanced kernel does not take (fewer than
+// 16 rows a CU, or K above 33792; the dot4 or K-split MFMA kernel by M) up to
 // their int32 partial sums: `part` gets [slices][M][N], slices being returned by
 // gemv_part_slices, and holds that many.
 int gemv_part_slices(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
@@ -100,7 +101,7 @@ hipError_t launch_gemv_part(const int8_t* x_i8, const uint8_t* packed, const int
 
 // ternary_gated_linear for decode batches (M <= 24) of a packed weight of N = 2 I
 // interleaved rows: the row-balanced kernel with whole pairs of rows to a
-// workgroup, or, for narrower layers, launch_gemv_part and a finishing kernel.
+// workgroup, or, where it does not apply, launch_gemv_part and a finishing kernel.
 size_t gemv_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
 hipError_t launch_gemv_gated(const int8_t* x_i8, const float* a_scale, const uint8_t* packed,
                              const int8_t* q, const float* smax, int64_t M, int64_t N, int64_t K,

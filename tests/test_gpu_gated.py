@@ -173,6 +173,22 @@ def test_python_refusals(twl):
     assert f(x[:0], a[:0], *w).shape == (0, 64)
 
 
+# rows of more than 33 groups a wave (K above 33792) leave the row-balanced kernel at
+# any width: partial sums of slices of K and the finishing kernel
+@pytest.mark.parametrize("M,N,K", [(1, 2048, 34816), (4, 2051, 34816), (24, 2048, 34816), (1, 2049, 65536), (24, 2048, 65536)])
+def test_long_rows_of_wide_layers(twl, M, N, K):
+    c = _case(M + K, M, N, K)
+    w = _pack(twl, c)
+    x, a = dev(c["x_i8"]), dev(c["a_scale"])
+    assert twl.gated_workspace_bytes(M, N, K) >= 2 * M * 2 * N * 4  # two slices at least
+    announce(f"gated M={M} N={N} K={K}")
+    out = twl.ternary_gated_linear(x, a, *w, out_dtype=torch.float32)
+    _check(out, *_want(c))
+    announce(f"gated M={M} N={N} K={K} GEMM")
+    assert torch.equal(twl.ternary_gated_linear(x, a, *w, out_dtype=torch.float32, path=twl.PATH_GEMM), out)
+    assert torch.equal(twl.ternary_gated_linear(x, a, *w), out.bfloat16())
+
+
 @pytest.mark.parametrize("M,N", [(24, 4), (24, 2048), (4096, 4)])
 def test_silu_bound(twl, M, N):
     """The bound that twl.h states for the activation, (1.25 |g| + 8) 2^-24, with g

@@ -423,8 +423,9 @@ hipError_t launch_blocks(const NormArgs& a, const DeviceInfo& dev, hipStream_t s
   // half the waves 226; 4096 of 12288 256 against 291).  The exception is the norm alone,
   // whose few operands leave the registers to two blocks a wave: 8192 of 8192 240 ->
   // 233 us, of 5120 159 -> 146.
-  if (!BRANCH && nblocks <= 8 && a.M > 3 * dev.cu_count)
-    return launch_form<2, ROT, BRANCH, false, 256, 3>(a, dev, stream);
+  if constexpr (!BRANCH) {
+    if (nblocks <= 8 && a.M > 3 * dev.cu_count) return launch_form<2, ROT, false, false, 256, 3>(a, dev, stream);
+  }
   if (nblocks <= 16) return launch_form<1, ROT, BRANCH, true, 1024, 4>(a, dev, stream);
   // two up to 24 (17408: one token 9.6 us, 2048 109; four a wave 14.5 and 149), then
   // four, in more registers (28672: 98 us against 106) while 12 waves hold the row

@@ -33,3 +33,22 @@ def test_no_scratch(tmp_path_factory, src, kernels):
     found = {k: int(v) for k, v in sizes.items() if re.search(kernels, k)}
     assert len(found) >= 8
     assert not any(found.values()), {k: v for k, v in found.items() if v}
+
+
+def _scratch(text):
+    return {k: int(v) for k, v in
+            re.findall(r"\.amdhsa_kernel (\S+)\n(?:.*\n)*?\s*\.amdhsa_private_segment_fixed_size (\d+)", text)}
+
+
+def test_lora_token_kernel_has_no_scratch(tmp_path_factory):
+    sizes = {k: v for k, v in _scratch(_compile_asm(tmp_path_factory, "lora.hip")).items() if "lora_token_kernel" in k}
+    assert len(sizes) == 2 and not any(sizes.values()), sizes
+
+
+def test_norm_forms_that_are_launched(tmp_path_factory):
+    """The split for many tokens of the norm alone (two blocks a wave, 256 threads) is
+    built without a branch only."""
+    names = _scratch(_compile_asm(tmp_path_factory, "norm_rotate.hip"))
+    forms = [re.search(r"norm_rotate_kernelILi(\d)ELb(\d)ELb(\d)ELb(\d)ELi(\d+)E", k).groups() for k in names]
+    assert len(forms) == 18
+    assert sorted(f for f in forms if f[4] == "256") == [("2", "0", "0", "0", "256"), ("2", "1", "0", "0", "256")]

@@ -4,7 +4,8 @@ their entry points in include/twl.h (argument checks and marshalling only).
 Tensors must be contiguous CUDA (HIP) tensors on the current device (but for
 the rows of norm_rotate_quant_act's gate); bf16 arguments may also be given as
 their int16 bit patterns.  Outputs and workspaces that a call allocates belong to
-the stream the call runs on.
+the stream the call runs on.  No operator has a backward pass: a tensor that
+requires grad is refused unless gradients are off (torch.no_grad()).
 """
 from __future__ import annotations
 
@@ -45,7 +46,7 @@ def _env():
 def _check(t, name, shape, dtypes, device):
     """The device pointer of a tensor argument of this shape on this device."""
     try:
-        if t.get_device() == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        if t.get_device() == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous() and not t.requires_grad:
             return t.data_ptr()
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor") from None
@@ -57,7 +58,11 @@ def _check(t, name, shape, dtypes, device):
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if _env().torch.is_grad_enabled():
+        raise ValueError(f"{name} requires grad, which this operator does not compute: detach it or call under torch.no_grad()")
+    return t.data_ptr()
 
 
 def _check_rows(t, name, shape, dtypes, device):

@@ -170,3 +170,32 @@ def test_gated_empty_calls_and_pack(lib):
     assert pack(P[0], P[1], P[2], P[3] + 2, 8, 1024, P[4], P[5], P[6], None, None) == EALIGN
     assert pack(P[0], P[1], P[2], P[3], 8, 1024, P[4], P[5], P[6], P[7] + 2, None) == EALIGN
     assert lib.twl_gated_workspace_bytes(4, 64, 1000) == 0
+
+
+def test_tensors_that_require_grad_are_refused():
+    """The operators have no backward pass: a result without a graph would lose an
+    adapter's gradients without a word.  With gradients off the call goes through."""
+    torch = pytest.importorskip("torch")
+    from ternary_weight_linear_block_amd import block
+
+    class OnGpu:  # what _check asks of a tensor
+        def __init__(self, t):
+            self.t, self.is_cuda, self.device = t, True, "cuda:0"
+
+        def get_device(self):
+            return 0
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+    w = torch.nn.Parameter(torch.zeros((3, 8), dtype=torch.bfloat16))
+    args = ("lora_a", (3, 8), (torch.bfloat16,), 0)
+    with pytest.raises(ValueError, match="lora_a requires grad"):
+        block._check(OnGpu(w), *args)
+    with pytest.raises(ValueError, match="has shape"):
+        block._check(OnGpu(w), "lora_a", (3, 9), (torch.bfloat16,), 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        block._check(OnGpu(w.t()), "lora_a", (8, 3), (torch.bfloat16,), 0)
+    with torch.no_grad():
+        assert block._check(OnGpu(w), *args) == w.data_ptr()
+    assert block._check(OnGpu(w.detach()), *args) == w.data_ptr()

@@ -247,3 +247,18 @@ def test_one_launch(twl, M, N, K, R, dtype):
     assert torch.all(buf[M:] == 7.0).item()
     y = c["y"].clone()
     _check(twl.lora_add(**dict(c, out=c["y"])), c, y=y)
+
+
+def test_gradients_are_refused(twl):
+    """Adapters that are being trained: no result without a graph; with gradients off
+    the same call gives the values."""
+    c = _case(2, 5, 64, 256, 16, 2, F32, [0, 1, 0, -1, 1])
+    announce("lora grad")
+    for name in ("y", "x", "lora_a", "lora_b", "scale"):
+        leaf = dict(c, **{name: c[name].detach().clone().requires_grad_()})
+        with pytest.raises(ValueError, match=f"{name} requires grad"):
+            twl.lora_add(**leaf)
+        with torch.no_grad():
+            _check(twl.lora_add(**leaf), c)
+        with torch.inference_mode():
+            _check(twl.lora_add(**leaf), c)

@@ -275,3 +275,23 @@ def test_products_outside_fp32_of_the_norm_alone(twl, M, K, x, weight):
         c[name] = W.f32_to_bf16_bits(W.bf16_bits_to_f32(c[name]) * np.float32(2.0 ** e))
     announce(f"norm alone, products M={M} x={x} weight={weight}")
     _check(_run(twl, c), c)
+
+
+def test_gradients_are_refused(twl):
+    c = _case(51, 3, 1024, True, True, "channel")
+    bf = {k: _t(c[k]).view(torch.bfloat16).requires_grad_() for k in ("x_bits", "weight_bits", "residual_bits", "post_bits", "gate_bits")}
+    announce("norm grad")
+
+    def run(**kw):
+        t = {k: v.detach() for k, v in bf.items()}
+        t.update(kw)
+        return twl.norm_rotate_quant_act(t["x_bits"], t["weight_bits"], dev(c["sign"]), eps=EPS, residual=t["residual_bits"],
+                                         post_weight=t["post_bits"], gate=t["gate_bits"], branch_scale=c["branch_scale"],
+                                         return_normed=True)
+
+    for k, v in bf.items():
+        with pytest.raises(ValueError, match="requires grad"):
+            run(**{k: v})
+    with torch.no_grad():
+        x_i8, a_scale, h, normed = run(**bf)
+    _check((x_i8, a_scale, h.view(torch.int16), normed.view(torch.int16)), c)

@@ -249,6 +249,47 @@ def test_one_launch(twl, M, N, K, R, dtype):
     _check(twl.lora_add(**dict(c, out=c["y"])), c, y=y)
 
 
+# M, N and rank of the two kernels (16 and 64 tokens a tile, each number of rank steps)
+TWO_KERNELS = [(20, 72, 32), (80, 1003, 64), (300, 72, 16), (300, 1032, 128)]
+
+
+@pytest.mark.parametrize("M,N,R", TWO_KERNELS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_nan_stays_with_its_users_two_kernels(twl, M, N, R, dtype):
+    """NaN and infinities in one adapter, one token, one row of y and the unused
+    adapter reach their own tokens' rows only, through both products' tiles."""
+    ids = [t % 4 if t % 7 else -1 for t in range(M)]
+    c = _case(M, M, N, 256, R, 5, dtype, ids)
+    c["lora_a"][2, 3, 7] = float("nan")
+    c["lora_b"][2, :, 1] = float("inf")
+    c["lora_a"][4] = float("nan")
+    c["lora_b"][4] = float("nan")
+    c["x"][5] = float("inf")
+    c["y"][9] = float("nan")
+    assert twl.lora_workspace_bytes(M, 256, R, 5) > 0
+    announce(f"lora nan M={M} N={N} R={R} {dtype}")
+    out = twl.lora_add(**c)
+    fine = [t for t in range(M) if ids[t] != 2 and t not in (5, 9)]
+    c["y"][9] = 0
+    out[9] = 0
+    with np.errstate(invalid="ignore"):
+        _check(out, dict(c, ids=torch.where(torch.arange(M, device="cuda") == 9, 0, c["ids"])), rows=fine)
+    assert not torch.isfinite(out[2]).any() and not torch.isfinite(out[5]).all()
+
+
+@pytest.mark.parametrize("M,N,R", TWO_KERNELS)
+def test_rows_and_workspace_behind_the_last_stay(twl, M, N, R):
+    c = _case(M, M, N, 256, R, 3, BF, mixed)
+    need = twl.lora_workspace_bytes(M, 256, R, 3)
+    assert need > 0
+    buf = torch.full((M + 3, N), 7.0, dtype=BF, device="cuda")
+    ws = torch.full((need + 64,), 0x7F, dtype=torch.uint8, device="cuda")
+    announce(f"lora guards M={M} N={N} R={R}")
+    _check(twl.lora_add(out=buf[:M], workspace=ws, **c), c)
+    assert torch.all(buf[M:] == 7.0).item()
+    assert torch.all(ws[need:] == 0x7F).item()
+
+
 def test_gradients_are_refused(twl):
     """Adapters that are being trained: no result without a graph; with gradients off
     the same call gives the values."""

@@ -287,9 +287,29 @@ def run_layer_steps(torch, twl, x, sign, sets, steps, warmup, kernel_iters=50, b
     return ms_step, ms_graph, rq, lin, extra
 
 
+def kernel_sources(kernel_src: str):
+    """A kernel's source file and the headers beside it that it includes, directly
+    or not."""
+    found, todo = [], [kernel_src]
+    while todo:
+        name = todo.pop()
+        path = os.path.join(ROOT, "ternary_weight_linear_block_amd", "csrc", name)
+        if name in found or not os.path.exists(path):
+            continue
+        found.append(name)
+        todo += [ln.split('"')[1] for ln in open(path) if ln.startswith('#include "')]
+    return found
+
+
+def kernel_traffic(kernel_src: str, workload: str):
+    """traffic_for where it holds for every source the kernel is compiled from."""
+    figures = {traffic_for(src, workload) for src in kernel_sources(kernel_src)}
+    return figures.pop() if len(figures) == 1 else None
+
+
 def traffic_for(kernel_src: str, workload: str):
     """HBM bytes per launch from the committed rocprofv3 counter summary, if
-    it was taken on the current kernel source (else None)."""
+    it was taken on the current version of this one source file (else None)."""
     path = os.path.join(ROOT, "profiles", "traffic.txt")
     src = os.path.join(ROOT, "ternary_weight_linear_block_amd", "csrc", kernel_src)
     if not (os.path.exists(path) and os.path.exists(src)):
@@ -730,7 +750,7 @@ def main(argv=None) -> int:
     plan = head["linear_plan"]
     roofline = {"bound": "mfma", "achieved": round(achieved, 2), "peak": PEAK_INT8_TOPS,
                 "unit": "TOP/s", "frac": round(achieved / PEAK_INT8_TOPS, 4),
-                "traffic": traffic_for("gemm_i8.hip", "prefill_gate_up"),
+                "traffic": kernel_traffic("gemm_i8.hip", "prefill_gate_up"),
                 "kernel": f"gemm_kernel ({plan['tile_rows']}x{plan['tile_cols']} tiles, "
                           f"{plan['workgroups']} workgroups, ternary_linear GEMM path)",
                 "algorithmic_ops_per_launch": ops,
@@ -760,7 +780,7 @@ def main(argv=None) -> int:
                            "workload": f"decode_gate_up M=1 K={dl['K']} N={dl['N']}",
                            "achieved": g1["weight_gbs"], "peak": PEAK_HBM_GBS, "unit": "GB/s",
                            "frac": g1["hbm_frac"], "algorithmic_bytes_per_launch": weight_bytes(dl["N"], dl["K"]),
-                           "traffic": traffic_for("gemv.hip", "decode_gate_up_m1"),
+                           "traffic": kernel_traffic("gemv.hip", "decode_gate_up_m1"),
                            "dot4_peak_tops": dot4_peak, "by_layer_and_M": by}
     cpu = None
     if not args.no_cpu:

@@ -60,3 +60,35 @@ def test_bench_refuses_more_than_one_gpu():
     assert res.returncode == 2
     assert "one GPU" in res.stderr
     assert res.stdout.strip() == ""
+
+
+@pytest.mark.parametrize("src,workload,sources", [
+    ("gemm_i8.hip", "prefill_gate_up", {"gemm_i8.hip", "twl_internal.h"}),
+    ("gemv.hip", "decode_gate_up_m1", {"gemv.hip", "gemv_rows.h", "rotate_block.h", "twl_internal.h"}),
+])
+def test_kernel_traffic_needs_every_source(tmp_path, monkeypatch, src, workload, sources):
+    """The decode kernel stands in a header: an edit there, or in any header a kernel
+    includes, has to drop its figures as an edit of the source file does."""
+    import shutil
+
+    import bench
+    assert set(bench.kernel_sources(src)) == sources
+    row = next(r for r in _rows() if r[0] == src and r[1] == workload)
+    assert bench.kernel_traffic(src, workload) == float(row[3]) + float(row[4])
+    for name in sources:
+        root = tmp_path / name
+        csrc = root / "ternary_weight_linear_block_amd" / "csrc"
+        shutil.copytree(CSRC, csrc)
+        (root / "profiles").mkdir()
+        shutil.copy(TRAFFIC, root / "profiles")
+        with monkeypatch.context() as m:
+            m.setattr(bench, "ROOT", str(root))
+            assert bench.kernel_traffic(src, workload) == float(row[3]) + float(row[4])
+            with open(csrc / name, "a") as f:
+                f.write("// changed\n")
+            assert bench.kernel_traffic(src, workload) is None, name
+
+
+def test_report_uses_the_guarded_figure():
+    text = open(os.path.join(ROOT, "bench.py")).read()
+    assert text.count('"traffic": kernel_traffic(') == 2 and '"traffic": traffic_for(' not in text

@@ -684,9 +684,11 @@ constexpr int kSplitPassesM = 256;
 // tokens of 24 requests take 109 us with four, 127 with one (a tile in which one
 // request ends and the next begins takes twice as long); 1500 tokens of 16 adapters
 // in any order 112, and 136 with two; but 1000 tokens of rank 16 17 us with four and
-// 21.5 with eight.  Eight cost nothing where y is large (from 4 x 10^7 elements on:
-// the 4096 tokens above 109, and 337 instead of 500 us with 200 of them in decode,
-// each with an adapter of its own).
+// 21.5 with eight.  Eight cost nothing where y is large: the 4096 tokens above 109,
+// and 337 instead of 500 us with 200 of them in decode, each with an adapter of its
+// own.  The border, 4 x 10^7 elements of y, lies between those (7 x 10^7) and 4096 x
+// 5120 (2 x 10^7, rank 128: 89.1 us with either); 1500 x 5120 (8 x 10^6) takes 32.5
+// with four and 33.8 with eight in request order, 111.7 and 107.9 in any order.
 int passes_of(const LoraArgs& a, int tokens) {
   const int share = a.M <= kSplitPassesM ? 16 : a.M * a.N >= 40000000 ? 8 : 4;
   return static_cast<int>(std::min<int64_t>({share, a.M, std::max(1, a.n), tokens}));

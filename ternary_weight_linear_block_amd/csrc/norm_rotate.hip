@@ -22,7 +22,7 @@
 // Workgroups stay and take every gridDim.x-th token; with one block a wave the
 // next token's rows are loaded while this one is computed.
 //
-// 8192 tokens of 5120 with everything: 116 us, 4.0 TB/s of the 461 MB that have to
+// 8192 tokens of 5120 with everything: 115 us, 4.0 TB/s of the 461 MB that have to
 // move (a copy reaches 5.15): the fp64 and rotation instructions, 2300 cycles a
 // block, take as long as the memory and overlap it in part.  333 tokens of 17408,
 // the norm alone: 12.8 us, the instructions of the CUs that have two tokens.  One

@@ -419,6 +419,114 @@ twl_status twl_ternary_gated_linear(const int8_t* x_i8, const float* a_scale, co
 /* Bytes of workspace twl_ternary_gated_linear may need on the current device. */
 size_t twl_gated_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+/*
+ * int8_linear -- the product with a weight that is held in 8 bits, beside the ternary
+ * one (projections that are not ternary: an output head, first and last layers):
+ *   acc[t,n] = sum_k x_i8[t,k] w_i8[n,k]                             (exact int32)
+ *   y[t,n]   = acc[t,n] * a_scale[t] * w_scale[n] + bias[n]           (fp32)
+ * with one scale for each token and one for each channel.  x_i8 and a_scale are what
+ * rotate_quant_act and its relatives leave; a weight [N, K] for them is made by the same
+ * call, rotate_quant_act of its rows with the layer's sign table (w_i8, w_scale).
+ * acc is rounded to fp32 before the products, each of which is rounded once, in the
+ * order above; bf16 rounds that value once more.
+ *   x_i8 in: int8 [M, K];  a_scale in: fp32 [M]
+ *   w_i8 in: int8 [N, K];  w_scale in: fp32 [N];  bias in: fp32 [N], or NULL
+ *   out  out: [M, N] by out_kind (TWL_OUT_F32, TWL_OUT_BF16, or TWL_OUT_ACC_I32: acc;
+ *             a_scale and w_scale are then ignored and a bias is TWL_EINVAL)
+ *   workspace: twl_int8_workspace_bytes(M, N, K) bytes, contents on entry do not
+ *             matter; calls sharing one must not run concurrently
+ * K is a positive multiple of 16 (not 1024) up to TWL_MAX_K; any int8 values, -128 too;
+ * M and N up to TWL_INT8_MAX_ROWS each, M N up to TWL_INT8_MAX_OUT.  An output that
+ * overlaps an input or the workspace is TWL_EINVAL.  Scales and biases that are not
+ * finite affect their own token or channel only.
+ */
+#define TWL_INT8_MAX_ROWS (1 << 24)
+#define TWL_INT8_MAX_OUT ((int64_t)1 << 33)
+twl_status twl_int8_linear(const int8_t* x_i8, const float* a_scale, const int8_t* w_i8, const float* w_scale,
+                           const float* bias, int64_t M, int64_t N, int64_t K, void* out, int out_kind,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace twl_int8_linear needs on the current device (0 where it needs none,
+ * and for invalid sizes). */
+size_t twl_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * qk_norm_rope -- between a block's query/key/value projection and its attention: RMSNorm
+ * of every query and key head, the position rotation, keys and values into the pages of
+ * a cache.  A row of qkv holds n_q query heads, n_kv key heads and n_kv value heads of D
+ * elements.  Per head, in fp32:
+ *   n = x / sqrt(mean(x^2) + eps) * weight         (a NULL weight: n = x for those heads)
+ *   rotated with c, s = cos_sin[p][i], cos_sin[p][rot/2 + i], p = positions[t]:
+ *   n'[i] = n[i] c - n[j] s,  n'[j] = n[j] c + n[i] s   for i < rot/2, where j = i + rot/2
+ *     (interleaved = 1: pairs 2i, 2i + 1 in place of i, j)
+ * elements from rot on, and values, stay as they are; one rounding to bf16 at the end.
+ *   qkv       in : fp32 or bf16 (kind: TWL_OUT_F32 or TWL_OUT_BF16), row t at
+ *                  qkv + t * row_stride elements (a multiple of 8, at least the width)
+ *   q_weight, k_weight in: bf16 [D], or NULL
+ *   cos_sin   in : fp32 [n_pos, rot], cosines then sines (best formed in 64 bits);
+ *                  ignored, as are the positions, when rot is 0 (no rotation)
+ *   positions in : int32 [M]; a token whose position is outside 0 .. n_pos-1 is
+ *                  padding: nothing is written for it
+ *   slots     in : int32 [M], page * page_size + place in the page; a token whose slot is
+ *                  outside the cache gets its queries written only.  NULL: token t has
+ *                  slot t (with page = 1 the caches are then k and v as [M, n_kv, D]).
+ *                  Two tokens of one slot leave any mixture of the two in it.
+ *   q         out: bf16 [M, n_q, D]
+ *   k_cache, v_cache out: bf16 [n_pages, n_kv, page, D]; slots of no token keep theirs
+ * D is 64, 128 or 256; n_q a multiple of n_kv of at most TWL_MAX_HEADS; rot a multiple
+ * of 16 up to D; page a power of two from 1 to 1024, at most 2^31 - 1 slots.  Outputs that
+ * overlap an input or each other are TWL_EINVAL.  A value that is not finite reaches its
+ * own head only.  Sums of squares beyond fp32's range give unspecified results.
+ */
+#define TWL_MAX_HEADS 1024
+twl_status twl_qk_norm_rope(const void* qkv, int kind, int64_t row_stride, const uint16_t* q_weight,
+                            const uint16_t* k_weight, double eps, const float* cos_sin, int64_t n_pos, int64_t rot,
+                            int interleaved, const int32_t* positions, const int32_t* slots, int64_t M, int64_t n_q,
+                            int64_t n_kv, int64_t D, uint16_t* q, uint16_t* k_cache, uint16_t* v_cache,
+                            int64_t n_pages, int64_t page, hipStream_t stream);
+
+/*
+ * window_attention -- causal attention of new tokens over the pages that qk_norm_rope
+ * fills, with a sliding window and a few first tokens that stay visible (sinks).
+ * Sequence b has kv_len[b] tokens in the cache, of which the last
+ * n = q_start[b+1] - q_start[b] are the new ones, rows q_start[b] .. of q; new token i is
+ * at position p = kv_len[b] - n + i.  With g = n_q / n_kv, query head h reads key head h / g:
+ *   sees(p, j) = 0 <= j <= p and (window == 0 or p - j < window or j < sinks)
+ *   out[t,h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j - max)   over sees(p, j)
+ * Scores, maximum and sums are fp32; a weight is rounded to bf16 for its product (the
+ * sum adds the rounded weights); out is rounded once.  A row that sees nothing
+ * (p < 0, say) is 0.
+ *   q          in : bf16 [T, n_q, D]
+ *   k_cache, v_cache in: bf16 [n_pages, n_kv, page, D]
+ *   page_table in : int32 [B, table_pages]: key j of sequence b lies in page
+ *                   page_table[b][j / page].  Keys beyond the table, or whose page is
+ *                   outside 0 .. n_pages-1 (a freed one, -1 say), are not seen.
+ *   q_start    in : int32 [B + 1], from 0, not decreasing; rows of q from q_start[B] on
+ *                   have no sequence: their out is left as it was.  Starts outside
+ *                   0 .. T are taken as the nearest of the two.
+ *   kv_len     in : int32 [B] (below 0: 0)
+ *   out        out: bf16 [T, n_q, D]
+ *   workspace     : twl_attention_workspace_bytes of the same sizes, contents on entry do
+ *                   not matter; calls sharing one must not run concurrently
+ * D is 64, 128 or 256; n_q a multiple of n_kv of at most TWL_MAX_HEADS; page a power of
+ * two from 16 to 1024; window and sinks 0 to 2^30 (sinks matter with a window only);
+ * T n_q up to 2^27, B n_kv up to 2^22.  The lengths are read on the device only, so that a
+ * captured call serves other lengths of the same T, B and table.  Keys and values that
+ * no row of a sequence sees may hold anything; values that are not finite in one that
+ * some row sees may reach the sequence's other rows.  An output or workspace that overlaps
+ * an input is TWL_EINVAL.
+ */
+twl_status twl_window_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache,
+                                const int32_t* page_table, const int32_t* q_start, const int32_t* kv_len, double scale,
+                                int64_t window, int64_t sinks, int64_t T, int64_t B, int64_t n_q, int64_t n_kv,
+                                int64_t D, int64_t n_pages, int64_t page, int64_t table_pages, uint16_t* out,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace twl_window_attention needs on the current device (0 where it needs
+ * none, and for invalid sizes). */
+size_t twl_attention_workspace_bytes(int64_t T, int64_t B, int64_t n_q, int64_t n_kv, int64_t D, int64_t page,
+                                     int64_t table_pages, int64_t window, int64_t sinks);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* twl_last_error(void);
 

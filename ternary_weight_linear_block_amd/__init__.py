@@ -10,7 +10,9 @@ Three operations, each one call into the C ABI declared in include/twl.h
 The operators of the block around them are in block.py: norm_rotate_quant_act
 (norms, gate, residual and the rotation in one pass), ternary_gated_linear (gate
 and up projections, SiLU and product in one kernel) and lora_add (low-rank
-adapters of many requests beside a projection).
+adapters of many requests beside a projection).  Those of its attention half are in
+attention.py: int8_linear (projections held in 8 bits), qk_norm_rope (norms of query
+and key heads, position rotation, cache) and window_attention.
 
 PyTorch provides device memory and the current stream.  Tensors must be CUDA
 (HIP) tensors on the current device, contiguous; x is bf16 (or its int16 bit
@@ -33,6 +35,7 @@ __all__ = [
     "HBLOCK", "GROUP", "MAX_K", "library",
     "norm_rotate_quant_act", "lora_add", "lora_workspace_bytes", "pack_ternary_gated",
     "ternary_gated_linear", "gated_workspace_bytes",
+    "int8_linear", "int8_workspace_bytes", "qk_norm_rope", "window_attention", "attention_workspace_bytes",
 ]
 
 
@@ -341,3 +344,5 @@ def ternary_linear_acc(x_i8, packed, q, path: int = PATH_AUTO, out=None, workspa
 # the block operators around the linear layer
 from .block import (gated_workspace_bytes, lora_add, lora_workspace_bytes, norm_rotate_quant_act,  # noqa: E402
                     pack_ternary_gated, ternary_gated_linear)
+from .attention import (attention_workspace_bytes, int8_linear, int8_workspace_bytes, qk_norm_rope,  # noqa: E402
+                        window_attention)

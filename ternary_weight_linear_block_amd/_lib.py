@@ -52,6 +52,13 @@ SIGNATURES = [
     ("twl_ternary_gated_linear", _INT,
      [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _INT, _INT, _P, _SIZE, _P]),
     ("twl_gated_workspace_bytes", _SIZE, [_I64, _I64, _I64]),
+    ("twl_int8_linear", _INT, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _INT, _P, _SIZE, _P]),
+    ("twl_int8_workspace_bytes", _SIZE, [_I64, _I64, _I64]),
+    ("twl_qk_norm_rope", _INT,
+     [_P, _INT, _I64, _P, _P, _F64, _P, _I64, _I64, _INT, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _P]),
+    ("twl_window_attention", _INT,
+     [_P, _P, _P, _P, _P, _P, _F64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _SIZE, _P]),
+    ("twl_attention_workspace_bytes", _SIZE, [_I64] * 9),
     ("twl_last_error", ctypes.c_char_p, []),
     ("twl_abi_version", _INT, []),
 ]

@@ -28,7 +28,8 @@ PEAKS_SRC = "peaks.hip"
 PEAKS_LIB_PATH = os.path.join(PKG_DIR, "libtwl_peaks.so")
 
 SOURCES = ["rotate_quant.hip", "pack.hip", "gemm_i8.hip", "gemv.hip", "gemv_gated.hip", "reference_bf16.hip",
-           "norm_rotate.hip", "lora.hip", "api.cpp", "api_block.cpp"]
+           "norm_rotate.hip", "lora.hip", "int8_linear.hip", "qk_rope.hip", "attention.hip", "api.cpp", "api_block.cpp",
+           "api_attention.cpp"]
 
 ARCH = "gfx950"
 COMMON_FLAGS = [

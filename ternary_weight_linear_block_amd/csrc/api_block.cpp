@@ -10,25 +10,6 @@ namespace {
 
 using namespace twl::api;
 
-// A byte range an argument covers; empty for a null pointer.
-struct Range {
-  const void* p;
-  size_t bytes;
-  const char* name;
-};
-
-bool overlap(const Range& a, const Range& b) {
-  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
-  const auto pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
-  return pa < pb + b.bytes && pb < pa + a.bytes;
-}
-
-// As TWL_REQUIRE_PTR for an argument that may be NULL.
-#define TWL_OPTIONAL_PTR(p)                                                                     \
-  do {                                                                                          \
-    if (!aligned16(p)) return fail(TWL_EALIGN, "%s is not 16-byte aligned", #p);                \
-  } while (0)
-
 twl_status check_lora(int64_t M, int64_t K, int64_t R, int64_t n) {
   TWL_TRY(check_rows("M", M));
   TWL_TRY(check_rows("n_adapters", n));

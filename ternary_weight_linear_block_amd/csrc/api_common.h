@@ -105,5 +105,24 @@ inline twl_status check_workspace(size_t need, const void* workspace, size_t wor
   return TWL_OK;
 }
 
+// A byte range an argument covers; empty for a null pointer.
+struct Range {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+
+inline bool overlap(const Range& a, const Range& b) {
+  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
+  const auto pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  return pa < pb + b.bytes && pb < pa + a.bytes;
+}
+
+// As TWL_REQUIRE_PTR for an argument that may be NULL.
+#define TWL_OPTIONAL_PTR(p) \
+  do { \
+    if (!twl::api::aligned16(p)) return twl::api::fail(TWL_EALIGN, "%s is not 16-byte aligned", #p); \
+  } while (0)
+
 }  // namespace api
 }  // namespace twl

@@ -1,0 +1,131 @@
+// qk_norm_rope: RMSNorm of every query and key head of a fused projection's output,
+// the position rotation, queries to a dense tensor, keys and values to the pages of
+// a cache (include/twl.h).
+//
+//   n = x / sqrt(mean(x^2) + eps) w                    per head of D elements, fp32
+//   (a, b) -> (a c - b s, b c + a s)                   pairs of the first `rot` elements
+//
+// A head's D <= 256 squares are summed in fp32 (relative error below 2^-20, against
+// the 2^-9 of the one rounding to bf16 at the end).
+//
+// Split: a wave takes 512 elements of a token's row at a time, 8 a lane, so that a head
+// is D / 8 adjacent lanes and a lane keeps its place in the head: weights are loaded
+// once for all of a wave's pieces, the token's cosines and sines once for each token.
+// The partner of a pair lies rot / 16 lanes away (or in the lane itself where pairs are
+// adjacent).  Every access is 16 bytes a lane; heads of the cache are whole runs of
+// 2 D bytes.
+#include "attention_internal.h"
+
+namespace twl {
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v8f __attribute__((ext_vector_type(8)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
+  constexpr int L = D / 8;          // lanes of a head
+  constexpr int HEADS = 512 / D;    // heads of a wave's piece
+  const int lane = threadIdx.x & 63;
+  const uint32_t item = blockIdx.x * 4u + (threadIdx.x >> 6);
+  const uint32_t token = item / a.parts, part = item % a.parts;
+  if (token >= a.M) return;
+  const int li = lane % L, d0 = li * 8;
+  int pos = 0;
+  if (a.rot > 0) {
+    pos = a.positions[token];
+    if (pos < 0 || pos >= a.n_pos) return;  // padding: nothing of this token is written
+  }
+  const int64_t slot = a.slots != nullptr ? a.slots[token] : static_cast<int64_t>(token);
+  const bool keep = slot >= 0 && slot < a.n_slots;
+
+  v8f wq = 1.0f, wk = 1.0f;
+  if (a.q_weight != nullptr) wq = __builtin_convertvector(*reinterpret_cast<const v8bf*>(a.q_weight + d0), v8f);
+  if (a.k_weight != nullptr) wk = __builtin_convertvector(*reinterpret_cast<const v8bf*>(a.k_weight + d0), v8f);
+  // the lane's eight cosines and sines; identity outside the rotated part
+  v8f c = 1.0f, s = 0.0f;
+  const int half = a.rot / 2;
+  const bool turns = d0 < a.rot;
+  int partner = lane;
+  if (turns) {
+    const float* row = a.cos_sin + static_cast<int64_t>(pos) * a.rot;
+    if (a.interleaved) {
+      const v4f c4 = *reinterpret_cast<const v4f*>(row + d0 / 2), s4 = *reinterpret_cast<const v4f*>(row + half + d0 / 2);
+      c = __builtin_shufflevector(c4, c4, 0, 0, 1, 1, 2, 2, 3, 3);
+      s = __builtin_shufflevector(s4, s4, 0, 0, 1, 1, 2, 2, 3, 3);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) s[i] = -s[i];
+    } else {
+      const bool low = d0 < half;
+      const int at = low ? d0 : d0 - half;
+      c = *reinterpret_cast<const v8f*>(row + at);
+      s = *reinterpret_cast<const v8f*>(row + half + at);
+      if (low) s = -s;
+      partner = low ? lane + half / 8 : lane - half / 8;
+    }
+  }
+  const int heads = a.n_q + 2 * a.n_kv;
+  const int64_t page = slot >> a.page_shift, off = slot & ((1 << a.page_shift) - 1);
+  for (uint32_t piece = part; piece * HEADS < static_cast<uint32_t>(heads); piece += a.parts) {
+    const int head = static_cast<int>(piece) * HEADS + lane / L;
+    const bool in = head < heads;
+    v8f x = 0.0f;
+    if (in) {
+      const int64_t at = static_cast<int64_t>(token) * a.stride + head * D + d0;
+      if (F32)
+        x = *reinterpret_cast<const v8f*>(static_cast<const float*>(a.qkv) + at);
+      else
+        x = __builtin_convertvector(*reinterpret_cast<const v8bf*>(static_cast<const uint16_t*>(a.qkv) + at), v8f);
+    }
+    const bool is_q = head < a.n_q, is_v = head >= a.n_q + a.n_kv;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(x[i], x[i], sum);
+#pragma unroll
+    for (int m = 1; m < L; m *= 2) sum += __shfl_xor(sum, m);
+    const float r = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
+    const bool norm = is_q ? a.q_weight != nullptr : a.k_weight != nullptr;
+    v8f n = x;
+    if (norm) n = x * r * (is_q ? wq : wk);
+    v8f other;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) other[i] = a.interleaved ? n[i ^ 1] : __shfl(n[i], partner);
+    v8f y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(n[i], c[i], other[i] * s[i]);
+    if (!turns) y = n;
+    if (is_v) y = x;
+    const v8bf out = __builtin_convertvector(y, v8bf);
+    if (!in) continue;
+    if (is_q) {
+      *reinterpret_cast<v8bf*>(a.q + (static_cast<int64_t>(token) * a.n_q + head) * D + d0) = out;
+    } else if (keep) {
+      const int h = is_v ? head - a.n_q - a.n_kv : head - a.n_q;
+      const int64_t at = (((page * a.n_kv + h) << a.page_shift) + off) * D + d0;
+      *reinterpret_cast<v8bf*>((is_v ? a.v_cache : a.k_cache) + at) = out;
+    }
+  }
+}
+
+template <int D>
+hipError_t launch_d(const RopeArgs& a, bool f32, uint32_t blocks, hipStream_t stream) {
+  if (f32)
+    qk_rope_kernel<D, true><<<blocks, 256, 0, stream>>>(a);
+  else
+    qk_rope_kernel<D, false><<<blocks, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_qk_rope(RopeArgs a, int D, bool f32, const DeviceInfo& dev, hipStream_t stream) {
+  const uint32_t pieces = static_cast<uint32_t>(((a.n_q + 2 * a.n_kv) * static_cast<int64_t>(D) + 511) / 512);
+  a.parts = pieces;
+  const uint32_t blocks = static_cast<uint32_t>((static_cast<int64_t>(a.M) * a.parts + 3) / 4);
+  if (D == 64) return launch_d<64>(a, f32, blocks, stream);
+  if (D == 128) return launch_d<128>(a, f32, blocks, stream);
+  return launch_d<256>(a, f32, blocks, stream);
+}
+
+}  // namespace twl

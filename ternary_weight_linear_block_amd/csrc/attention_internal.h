@@ -17,6 +17,7 @@ struct Int8Args {
   int32_t* part;      // holds int8_workspace_bytes
   int M, N, K;
   int kind;
+  int tiles_m, tiles_n, splits;  // set by the launcher
 };
 size_t int8_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
 hipError_t launch_int8(Int8Args a, const DeviceInfo& dev, hipStream_t stream);

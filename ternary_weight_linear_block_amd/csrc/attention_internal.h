@@ -40,7 +40,7 @@ struct RopeArgs {
 };
 hipError_t launch_qk_rope(RopeArgs a, int D, bool f32, const DeviceInfo& dev, hipStream_t stream);
 
-// window_attention (include/twl.h).  The caller sets everything but group and splits.
+// window_attention (include/twl.h).  The caller sets everything up to sinks.
 struct AttnArgs {
   const uint16_t* q;
   const uint16_t* k;
@@ -52,7 +52,8 @@ struct AttnArgs {
   float* part;               // holds attention_workspace_bytes
   float scale_log2;          // scale * log2(e)
   int T, B, n_q, n_kv, page_shift, n_pages, table_pages, window, sinks;
-  int group, splits;
+  int group, splits, large_splits, max_splits;  // set by the launcher, as what follows
+  int small_rows, large_rows, large_keys;
 };
 size_t attention_workspace_bytes(int64_t T, int64_t B, int n_q, int n_kv, int D, int64_t table_keys, int window, int sinks,
                                  const DeviceInfo& dev);

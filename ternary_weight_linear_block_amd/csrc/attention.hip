@@ -9,6 +9,7 @@
 #include "attention_internal.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace twl {
 namespace {
@@ -39,7 +40,13 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t offset, uint32_
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds_base) : "memory", "m0");
 }
 
-__device__ __forceinline__ void wait_vm0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits for this wave's loads, of either kind.  The builtin, not inline asm: the compiler then
+// knows that its own loads have landed and does not wait for them again behind later ones.
+__device__ __forceinline__ void wait_vm0() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x7 << 4 | 0xF << 8);  // vmcnt 0, the others as they are
+  asm volatile("" ::: "memory");
+}
 
 // Four elements of one column from four rows: within 16 lanes, lane l gives the address
 // of elements 4 (l % 4) .. + 3 of row l / 4 and receives column l of rows 0 .. 3.
@@ -57,30 +64,35 @@ struct Tile {
   int seen;           // keys that the page table holds, at most kv
 };
 
+// The last sequence whose start, scaled by `before(start, b)`, is not beyond what is looked
+// for: each lane looks at one sequence, and what the found one needs comes with it.
+template <class Before>
+__device__ __forceinline__ bool find_sequence(const AttnArgs& a, int lane, Tile* t, Before before) {
+  bool found = false;
+  for (int base = 0; base < a.B; base += 64) {
+    const int b = min(base + lane, a.B - 1);
+    const int start = a.q_start[b], end = a.q_start[b + 1], kv = a.kv_len[b];
+    const int q0 = min(max(start, 0), a.T);
+    const int here = __popcll(__ballot(base + lane < a.B && before(q0, b)));
+    if (here > 0) {
+      found = true;
+      t->seq = base + here - 1;
+      t->q0 = __builtin_amdgcn_readlane(q0, here - 1);
+      t->n = min(max(__builtin_amdgcn_readlane(end, here - 1), t->q0), a.T) - t->q0;
+      t->kv = max(__builtin_amdgcn_readlane(kv, here - 1), 0);
+    }
+    if (here < 64) break;
+  }
+  t->seen = a.n_pages > 0 ? static_cast<int>(min(static_cast<int64_t>(t->kv), static_cast<int64_t>(a.table_pages) << a.page_shift)) : 0;
+  return found;
+}
+
 // The sequence of tile `tile`: sequence b owns the tiles from floor(q_start[b] g / rows) + b,
 // which leaves it at least ceil(n g / rows) of them.  False for a tile without rows.
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, int rows, int lane, Tile* t) {
-  int count = 0;
-  for (int base = 0; base < a.B; base += 64) {
-    const int b = base + lane;
-    bool before = false;
-    if (b < a.B) {
-      const int64_t q0 = min(max(a.q_start[b], 0), a.T);
-      before = q0 * a.group / rows + b <= tile;
-    }
-    const int here = __popcll(__ballot(before));
-    count += here;
-    if (here < 64) break;
-  }
-  if (count == 0) return false;
-  const int b = count - 1;
-  t->seq = b;
-  t->q0 = min(max(a.q_start[b], 0), a.T);
-  t->n = min(max(a.q_start[b + 1], t->q0), a.T) - t->q0;
-  const int first = static_cast<int>(static_cast<int64_t>(t->q0) * a.group / rows) + b;
-  t->row0 = (tile - first) * rows;
-  t->kv = max(a.kv_len[b], 0);
-  t->seen = a.n_pages > 0 ? static_cast<int>(min(static_cast<int64_t>(t->kv), static_cast<int64_t>(a.table_pages) << a.page_shift)) : 0;
+  auto first = [&](int q0, int b) { return static_cast<int>(static_cast<int64_t>(q0) * a.group / rows) + b; };
+  if (!find_sequence(a, lane, t, [&](int q0, int b) { return first(q0, b) <= tile; })) return false;
+  t->row0 = (tile - first(t->q0, t->seq)) * rows;
   return t->row0 < t->n * a.group;
 }
 
@@ -153,8 +165,8 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
   constexpr int C = D / 32;                 // steps of 32 along D
   constexpr int DT = D / 16;                // tiles of 16 along D
   constexpr int ROW = 2 * D;                // bytes of a key
-  constexpr int VBYTES = kSmallKeys * ROW;  // a wave's block of V; later its 16 x D sums in fp32
-  __shared__ __attribute__((aligned(16))) char smem[kSmallWaves * VBYTES];
+  constexpr int VBYTES = kSmallKeys * ROW;  // a block of V; a wave has two, and later 16 x D sums in fp32 in the first
+  __shared__ __attribute__((aligned(16))) char smem[kSmallWaves * 2 * VBYTES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, h = lane >> 4;
   const int head = blockIdx.x % a.n_kv;
@@ -179,58 +191,83 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
 
   const int32_t* table = a.page_table + static_cast<int64_t>(t.seq) * a.table_pages;
   const int page_mask = (1 << a.page_shift) - 1;
-  char* vmem = smem + wave * VBYTES;
+  char* vmem = smem + wave * 2 * VBYTES;
   const uint32_t vbase = lds_addr(vmem);
+
+  // The wave's blocks: from + wave, four on each time.  A lane holds the page of 16 keys of one
+  // of the next 32 of them.
+  const int count = (to - from - wave + kSmallWaves - 1) / kSmallWaves;
+  auto key_of = [&](int it) {
+    const int i = from + wave + min(it, count - 1) * kSmallWaves;
+    return (i < k.sink ? i : i - k.sink + k.first) * kSmallKeys;
+  };
+  auto pages = [&](int it) { return table[min((key_of(it + (lane >> 1)) + (lane & 1) * 16) >> a.page_shift, a.table_pages - 1)]; };
+  struct Keys {
+    v8bf k[2][C];
+  } cur, next;
+  int ids = 0;
+  // a block's page ids; the keys 0 .. 15 and 16 .. 31 lie in a page each (or in one)
+  auto page_of = [&](int it, int sub) { return __builtin_amdgcn_readlane(ids, (it & 31) * 2 + sub); };
+  auto is_none = [&](int page) { return page < 0 || page >= a.n_pages; };
+  // V to LDS, 1 KB an instruction (a row's 32-byte units XOR-swizzled by the key), K to registers
+  auto load = [&](int it, Keys& to_k) {
+    if ((it & 31) == 0) ids = pages(it);
+    const int key0 = key_of(it), pg0 = page_of(it, 0), pg1 = page_of(it, 1);
+    const int64_t at0 = ((static_cast<int64_t>(is_none(pg0) ? 0 : pg0) * a.n_kv + head) << a.page_shift) + (key0 & page_mask);
+    const int64_t at1 = ((static_cast<int64_t>(is_none(pg1) ? 0 : pg1) * a.n_kv + head) << a.page_shift) + ((key0 + 16) & page_mask);
+#pragma unroll
+    for (int n = 0; n < VBYTES / 1024; ++n) {
+      const int byte = n * 1024 + lane * 16;
+      const int key = byte / ROW, unit = (byte % ROW) / 32;
+      const int swz = D == 64 ? key & 3 : (key & 3) | (key >> 1 & 4);
+      const char* base = reinterpret_cast<const char*>(a.v) + (n * 1024 / ROW < 16 ? at0 : at1 - 16) * ROW;  // an instruction's keys lie in one page
+      dma16(sgpr_ptr(base), key * ROW + (unit ^ swz) * 32 + (byte & 16), vbase + (it & 1) * VBYTES + n * 1024);
+    }
+    const int64_t at = m < 8 ? at0 + (m >> 2) * 8 + (m & 3) : at1 + (m >> 2) * 8 + (m & 3) - 16;
+    const uint16_t* kp = a.k + at * D + h * 8;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      to_k.k[0][c] = *reinterpret_cast<const v8bf*>(kp + c * 32);
+      to_k.k[1][c] = *reinterpret_cast<const v8bf*>(kp + 4 * D + c * 32);
+    }
+  };
 
   v4f o[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) o[d] = 0.0f;
   float mx = kNoMax, sum = 0.0f;
 
-  for (int i = from + wave; i < to; i += kSmallWaves) {
-    const int key0 = (i < k.sink ? i : i - k.sink + k.first) * kSmallKeys;
-    // the block lies in one page, or in two of 16 keys
-    const int e0 = key0 >> a.page_shift, e1 = (key0 + 16) >> a.page_shift;
-    int pg0 = table[min(e0, a.table_pages - 1)], pg1 = table[min(e1, a.table_pages - 1)];
-    const bool bad0 = pg0 < 0 || pg0 >= a.n_pages, bad1 = pg1 < 0 || pg1 >= a.n_pages;
-    if (bad0) pg0 = 0;
-    if (bad1) pg1 = 0;
-    const int64_t at0 = ((static_cast<int64_t>(pg0) * a.n_kv + head) << a.page_shift) + (key0 & page_mask);
-    const int64_t at1 = ((static_cast<int64_t>(pg1) * a.n_kv + head) << a.page_shift) + ((key0 + 16) & page_mask);
-    // V, 1 KB an instruction; a row's 32-byte units are XOR-swizzled by the key
-#pragma unroll
-    for (int n = 0; n < VBYTES / 1024; ++n) {
-      const int byte = n * 1024 + lane * 16;
-      const int key = byte / ROW, unit = (byte % ROW) / 32;
-      const int swz = D == 64 ? key & 3 : (key & 3) | (key >> 1 & 4);
-      const int64_t at = key < 16 ? at0 + key : at1 + (key - 16);
-      dma16(reinterpret_cast<const char*>(a.v) + at * ROW + (unit ^ swz) * 32 + (byte & 16), vbase + n * 1024);
-    }
+  if (count > 0) load(0, next);
+  for (int it = 0; it < count; ++it) {
+    const int key0 = key_of(it);
+    const bool bad0 = is_none(page_of(it, 0)), bad1 = is_none(page_of(it, 1));
+    wait_vm0();
+    cur = next;
+    if (it + 1 < count) load(it + 1, next);
     v4f s0 = 0.0f, s1 = 0.0f;
-    const int64_t at = m < 8 ? at0 + (m >> 2) * 8 + (m & 3) : at1 + (m >> 2) * 8 + (m & 3) - 16;
-    const uint16_t* kp = a.k + at * D + h * 8;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const v8bf k0 = *reinterpret_cast<const v8bf*>(kp + c * 32);
-      const v8bf k1 = *reinterpret_cast<const v8bf*>(kp + 4 * D + c * 32);
-      s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[c], s0, 0, 0, 0);
-      s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[c], s1, 0, 0, 0);
+      s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cur.k[0][c], q[c], s0, 0, 0, 0);
+      s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cur.k[1][c], q[c], s1, 0, 0, 0);
     }
     float s[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
     // keys past the last, before the window or in a page that is none
     const bool border = bad0 || bad1 || key0 + kSmallKeys - 1 > min(k.hi - 1, t.kv - t.n + t.row0 / a.group) ||
                         (a.window > 0 && key0 < t.kv - a.window);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] *= a.scale_log2;
+    if (border) {
+      const bool none = h < 2 ? bad0 : bad1;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = key0 + 8 * h + e;
+        const bool hidden = (j > p) | (j >= t.seen) | ((a.window > 0) & (p - j >= a.window) & (j >= a.sinks)) | none;
+        s[e] = hidden ? -__builtin_inff() : s[e];
+      }
+    }
     float top = mx;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      s[e] *= a.scale_log2;
-      if (border) {
-        const int j = key0 + 8 * h + e;
-        const bool sees = j <= p && j < t.seen && (a.window == 0 || p - j < a.window || j < a.sinks) && !(h < 2 ? bad0 : bad1);
-        s[e] = sees ? s[e] : -__builtin_inff();
-      }
-      top = fmaxf(top, s[e]);
-    }
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, s[e]);
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     const float alpha = __builtin_amdgcn_exp2f(mx - top);
@@ -245,7 +282,7 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
     sum = sum * alpha + part;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] *= alpha;
-    wait_vm0();
+    char* v = vmem + (it & 1) * VBYTES;
     if (border) {
       // what no row sees may hold anything: its weight 0 must meet a number
       const int key = lane >> 1;
@@ -254,7 +291,7 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
       if (dead)
 #pragma unroll
         for (int c = 0; c < ROW / 32; ++c)
-          *reinterpret_cast<v4f*>(vmem + key * ROW + (lane & 1) * (ROW / 2) + c * 16) = 0.0f;
+          *reinterpret_cast<v4f*>(v + key * ROW + (lane & 1) * (ROW / 2) + c * 16) = 0.0f;
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 #pragma unroll
@@ -264,7 +301,7 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
       for (int e = 0; e < 2; ++e) {
         const int key = h * 8 + e * 4 + (m >> 2);
         const int swz = D == 64 ? key & 3 : (key & 3) | (key >> 1 & 4);
-        half[e] = read_tr(vbase + key * ROW + (d ^ swz) * 32 + (m & 3) * 8);
+        half[e] = read_tr(vbase + (it & 1) * VBYTES + key * ROW + (d ^ swz) * 32 + (m & 3) * 8);
       }
       const v8bf vt = __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7);
       o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr, o[d], 0, 0, 0);
@@ -298,7 +335,7 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
     const int d = u * kSmallWaves + wave;
     v4f v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kSmallWaves; ++w) v += reinterpret_cast<const v4f*>(smem + w * VBYTES)[d * 64 + lane];
+    for (int w = 0; w < kSmallWaves; ++w) v += reinterpret_cast<const v4f*>(smem + w * 2 * VBYTES)[d * 64 + lane];
     if (!real) continue;
     if (whole)
       *reinterpret_cast<v4bf*>(a.out + out_row * D + d * 16 + h * 4) = __builtin_convertvector(v * inv, v4bf);
@@ -323,6 +360,12 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
 //
 // The maximum that weights refer to follows the scores' only when a row's grows by more than
 // 2^8 (weights stay below 2^8, sums far below fp32's range): most blocks leave O as it is.
+#ifndef PA
+#define PA
+#define PB
+#define PC
+#define PD
+#endif
 template <int D, int WAVES>
 struct Large {
   static constexpr int KT = D == 256 ? 1 : 2, KEYS = 32 * KT, ROWS = 32 * WAVES;
@@ -406,6 +449,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_large_
   const int vkey = 4 * half + (lane >> 2 & 3);                  // the lane's key of a transposing read, of 8
   const uint32_t k_read = lds + l32 * ROW, v_read = lds + L::TILE + vkey * ROW + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
 
+  PD
   int ids = 0, next_ids = 0;
   if (from < to) {
     ids = pages(from);
@@ -432,6 +476,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_large_
     // blocks that none of the wave's rows sees
     if (key0 > p_high || (a.window > 0 && key0 >= a.sinks && key0 + KEYS <= p_low - a.window + 1)) continue;
 
+    PA
     const uint32_t kb = k_read + (i & 1) * 2 * L::TILE, vb = v_read + (i & 1) * 2 * L::TILE;
     v16f s[KT];
 #pragma unroll
@@ -453,6 +498,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_large_
           s[x][r] = sees ? s[x][r] : -__builtin_inff();
         }
     }
+    PB
     float top = s[0][0];
 #pragma unroll
     for (int x = 0; x < KT; ++x)
@@ -478,6 +524,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_large_
         w[x][r >> 3][r & 7] = pair[0];
         w[x][r >> 3][(r & 7) + 1] = pair[1];
       }
+    PC
 #pragma unroll
     for (int x = 0; x < KT; ++x)
 #pragma unroll
@@ -513,40 +560,61 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_large_
   }
 }
 
-// The splits of every row of a tile joined: a wave a row.
+// The splits of a row joined: a workgroup a row, eight splits a wave, so that one wait (2 us for
+// sums that another XCD wrote) covers them all.  A wave a row with eight splits at a time took
+// 17 us for 64 splits, this 4; more than 32 splits were no faster (32768 keys: 34.9 us of 64, 34.1 of 32).
+constexpr int kMostSplits = 32;
+
 template <int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   constexpr int PER = D / 64;
+  typedef std::conditional_t<PER == 1, float, float __attribute__((ext_vector_type(PER == 1 ? 2 : PER)))> vec;
+  __shared__ vec joined[4][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int head = blockIdx.x % a.n_kv, quarter = blockIdx.x / a.n_kv % 4;
+  const int64_t rows = static_cast<int64_t>(a.T) * a.n_q, out_row = blockIdx.x;
+  // lane s: maximum and sum of split s; and the sums of the wave's first splits: loaded before it is
+  // known how many there are, which the lengths say (what was not written is not used)
+  const float* ml = a.part + a.max_splits * rows * D + (min(lane, a.max_splits - 1) * rows + out_row) * 2;
+  const float m_loaded = ml[0], l_loaded = ml[1];
+  const float* part = a.part + out_row * D + lane * PER;
+  vec v[8];
+#pragma unroll
+  for (int s = 0; s < 8; ++s) v[s] = *reinterpret_cast<const vec*>(part + min(wave * 8 + s, a.max_splits - 1) * rows * D);
   Tile t;
-  if (!find_tile(a, blockIdx.x / a.n_kv / 4, kSmallRows, lane, &t)) return;
+  const int token = static_cast<int>(out_row / a.n_q), qh = static_cast<int>(out_row % a.n_q);
+  if (!find_sequence(a, lane, &t, [&](int q0, int) { return q0 <= token; }) || token >= t.q0 + t.n) return;
+  const int row = (token - t.q0) * a.group + qh % a.group;
   int splits;
   if (t.n * a.group <= a.small_rows) {
+    t.row0 = row / kSmallRows * kSmallRows;
     splits = active_splits(a, find_blocks(a, t, kSmallRows, kSmallKeys).total);
   } else {
-    Tile large = t;
-    large.row0 = t.row0 / a.large_rows * a.large_rows;
-    splits = large_splits(a, find_blocks(a, large, a.large_rows, a.large_keys).total);
+    t.row0 = row / a.large_rows * a.large_rows;
+    splits = large_splits(a, find_blocks(a, t, a.large_rows, a.large_keys).total);
   }
-  const int row = t.row0 + quarter * 4 + wave;
-  if (splits == 1 || row >= t.n * a.group) return;
-  const int64_t rows = static_cast<int64_t>(a.T) * a.n_q;
-  const int64_t out_row = static_cast<int64_t>(t.q0 + row / a.group) * a.n_q + head * a.group + row % a.group;
-  const float* ml = a.part + a.max_splits * rows * D + out_row * 2;
-  float top = kNoMax;
-  for (int s = 0; s < splits; ++s) top = fmaxf(top, ml[s * rows * 2]);
-  float all = 0.0f, acc[PER] = {};
-  for (int s = 0; s < splits; ++s) {
-    const float w = __builtin_amdgcn_exp2f(ml[s * rows * 2] - top);
-    all += ml[s * rows * 2 + 1] * w;
+  if (splits == 1) return;
+  const float m = lane < splits ? m_loaded : kNoMax, l = lane < splits ? l_loaded : 0.0f;
+  float top = m;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] += a.part[(s * rows + out_row) * D + lane * PER + e] * w;
+  for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
+  const float mine = __builtin_amdgcn_exp2f(m - top);
+  float all = l * mine;
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) all += __shfl_xor(all, x);
+  vec acc = 0.0f;
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    if (wave * 8 + s < splits) acc += v[s] * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), wave * 8 + s));
+  joined[wave][lane] = acc;
+  __syncthreads();
+  if (wave != 0) return;
+  acc = (joined[0][lane] + joined[1][lane] + joined[2][lane] + joined[3][lane]) * (all > 0.0f ? 1.0f / all : 0.0f);
+  if constexpr (PER == 1) {
+    *reinterpret_cast<__bf16*>(a.out + out_row * D + lane) = static_cast<__bf16>(acc);
+  } else {
+    typedef __bf16 bvec __attribute__((ext_vector_type(PER == 1 ? 2 : PER)));
+    *reinterpret_cast<bvec*>(a.out + out_row * D + lane * PER) = __builtin_convertvector(acc, bvec);
   }
-  const float inv = all > 0.0f ? 1.0f / all : 0.0f;
-#pragma unroll
-  for (int e = 0; e < PER; ++e)
-    *reinterpret_cast<__bf16*>(a.out + out_row * D + lane * PER + e) = static_cast<__bf16>(acc[e] * inv);
 }
 
 int64_t tiles_of(const AttnArgs& a, int rows) { return static_cast<int64_t>(a.T) * a.group / rows + a.B; }
@@ -574,7 +642,7 @@ Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_k
   if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + kSmallRows + 2 * kSmallKeys);
   const int64_t most = std::max<int64_t>(1, (keys + kSmallKeys - 1) / kSmallKeys / kSplitBlocks);
   const int64_t tiles = std::max<int64_t>(1, std::min(T, T * group / kSmallRows + std::min(B, T))) * n_kv;
-  p.splits = !p.small ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, 32), 2 * dev.cu_count / tiles)));
+  p.splits = !p.small ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, kMostSplits), (D == 64 ? 12 : D == 128 ? 8 : 4) * dev.cu_count / tiles)));
   // many rows: 256 a workgroup where that still fills the device, else 128, and splits below that
   const int64_t rows = T * group * n_kv;
   p.waves = D < 256 && rows / 256 >= 2 * dev.cu_count ? 8 : 4;
@@ -607,7 +675,7 @@ hipError_t launch_d(AttnArgs a, const Plan& p, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   if (a.max_splits == 1) return hipSuccess;
-  attention_join_kernel<D><<<tiles * 4, 256, 0, stream>>>(a);
+  attention_join_kernel<D><<<static_cast<uint32_t>(a.T * a.n_q), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -349,8 +349,9 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
   }
 }
 
-// Many rows: a tile of 32 WAVES packed rows a workgroup, 32 of them a wave, whose waves
-// share each block of KT x 32 keys in LDS (two buffers, loaded a block ahead).
+// Many rows: a tile of 128 packed rows a workgroup, 32 of them a wave, whose waves share
+// each block of KT x 32 keys in LDS (two buffers, loaded a block ahead).  Two workgroups share a CU
+// (one for D = 256), so that one has its products while the other has its exponentials.
 //
 // S^T = K Q^T and O^T = V^T P^T on 32x32x16 MFMAs: a lane holds one row (lane % 32) in both,
 // so that maximum, sum and factors are a lane's own (and its partner's, 32 lanes on), and
@@ -360,15 +361,10 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
 //
 // The maximum that weights refer to follows the scores' only when a row's grows by more than
 // 2^8 (weights stay below 2^8, sums far below fp32's range): most blocks leave O as it is.
-#ifndef PA
-#define PA
-#define PB
-#define PC
-#define PD
-#endif
-template <int D, int WAVES>
+template <int D>
 struct Large {
-  static constexpr int KT = D == 256 ? 1 : 2, KEYS = 32 * KT, ROWS = 32 * WAVES;
+  static constexpr int WAVES = 4, ROWS = 32 * WAVES;
+  static constexpr int KT = D == 256 ? 1 : 2, KEYS = 32 * KT;
   static constexpr int ROW = 2 * D, CHUNKS = D / 8;             // bytes and 16-byte chunks of a key
   static constexpr int RPI = 1024 / ROW;                        // keys of a load instruction
   static constexpr int LOADS = KEYS / RPI / WAVES;              // load instructions of a wave for K, and for V
@@ -380,11 +376,11 @@ struct Large {
   __device__ static __forceinline__ int v_turn(int key) { return D == 64 ? key >> 1 & 1 : key & 3; }
 };
 
-template <int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_large_kernel(AttnArgs a) {
-  using L = Large<D, WAVES>;
+template <int D>
+__global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attention_large_kernel(AttnArgs a) {
+  using L = Large<D>;
   constexpr int KT = L::KT, KEYS = L::KEYS, ROW = L::ROW, DS = D / 16, DT = D / 32;
-  __shared__ __attribute__((aligned(16))) char smem[4 * L::TILE];  // K, V of two blocks
+  __shared__ __attribute__((aligned(16))) char smem[4 * L::TILE];  // K of two blocks, V of two
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, half = lane >> 5;
   const int head = blockIdx.x % a.n_kv, split = blockIdx.x / a.n_kv % a.large_splits;
@@ -402,7 +398,6 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_large_
   const int rows = t.n * a.group, first_row = t.row0 + wave * 32;
   const int row = min(first_row + l32, rows - 1), token = row / a.group;
   const int p = t.kv - t.n + token;
-  const int p_low = t.kv - t.n + min(first_row, rows - 1) / a.group, p_high = first_row < rows ? t.kv - t.n + min(first_row + 31, rows - 1) / a.group : -1;
   const int64_t out_row = static_cast<int64_t>(t.q0 + token) * a.n_q + head * a.group + row % a.group;
   const float scale = a.scale_log2 == 0.0f ? 1.0f : __builtin_fabsf(a.scale_log2);
   v8bf q[DS];
@@ -414,96 +409,120 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_large_
     q[c] = __builtin_bit_cast(v8bf, bits);
   }
 
+  // Blocks of which every row of the wave sees every key (none to mask), and those of which some row
+  // of the tile sees each (none to clean), as ranges of the tile's blocks; sinks' blocks are in neither.
+  const int p_low = t.kv - t.n + min(first_row, rows - 1) / a.group, p_high = t.kv - t.n + min(first_row + 31, rows - 1) / a.group;
+  auto block_of = [&](int b) { return max(b - k.first, 0) + k.sink; };  // the place of keys b KEYS .. in the tile's blocks
+  const int calm_from = block_of(a.window > 0 ? (max(p_high - a.window + 1, 0) + KEYS - 1) / KEYS : 0);
+  const int calm_to = block_of(max(min(p_low + 1, t.seen), 0) / KEYS);
+  const int whole_from = block_of((k.lo + KEYS - 1) / KEYS), whole_to = block_of(k.hi / KEYS);
+
   const int32_t* table = a.page_table + static_cast<int64_t>(t.seq) * a.table_pages;
   const int page_mask = (1 << a.page_shift) - 1;
   const uint32_t lds = lds_addr(smem);
   uint32_t k_off[L::LOADS], v_off[L::LOADS];
 #pragma unroll
   for (int i = 0; i < L::LOADS; ++i) {
-    const int key = (i * WAVES + wave) * L::RPI + lane / L::CHUNKS, chunk = lane % L::CHUNKS;
+    const int key = (i * L::WAVES + wave) * L::RPI + lane / L::CHUNKS, chunk = lane % L::CHUNKS;
     k_off[i] = lane / L::CHUNKS * ROW + L::k_place(key, chunk) * 16;
     v_off[i] = lane / L::CHUNKS * ROW + (chunk ^ L::v_turn(key) * 4) * 16;
   }
   auto key_of = [&](int i) { return (i < k.sink ? i : i - k.sink + k.first) * KEYS; };
-  // the pages of block i's keys, one a lane
+  // A block's keys, one a lane: the byte offset of each in the caches, and the lanes of those whose page is none.
   auto pages = [&](int i) { return table[min((key_of(min(i, to - 1)) + lane % KEYS) >> a.page_shift, a.table_pages - 1)]; };
-  auto load = [&](int i, int page_ids) {
-    const int key0 = key_of(i);
+  struct Where {
+    uint32_t lo, hi;
+    uint64_t none;
+  };
+  auto where = [&](int i, int page) {
+    Where w;
+    const bool bad = page < 0 || page >= a.n_pages;
+    w.none = __ballot(bad);
+    const uint64_t at = (static_cast<uint64_t>(static_cast<uint32_t>(bad ? 0 : page)) * static_cast<uint32_t>(a.n_kv << a.page_shift) +
+                         static_cast<uint32_t>((head << a.page_shift) + ((key_of(i) + lane % KEYS) & page_mask))) * ROW;
+    w.lo = static_cast<uint32_t>(at);
+    w.hi = static_cast<uint32_t>(at >> 32);
+    return w;
+  };
+  auto load = [&](const Where& w, const uint16_t* cache, const uint32_t (&off)[L::LOADS], uint32_t to_lds) {
 #pragma unroll
     for (int n = 0; n < L::LOADS; ++n) {
-      const int key = (n * WAVES + wave) * L::RPI;  // a load's keys lie in one page
-      int page = __builtin_amdgcn_readlane(page_ids, key);
-      if (page < 0 || page >= a.n_pages) page = 0;
-      const int64_t at = ((((static_cast<int64_t>(page) * a.n_kv + head) << a.page_shift) + ((key0 + key) & page_mask))) * ROW;
-      const uint32_t to_lds = lds + (i & 1) * 2 * L::TILE + key * ROW;
-      dma16(sgpr_ptr(reinterpret_cast<const char*>(a.k) + at), k_off[n], to_lds);
-      dma16(sgpr_ptr(reinterpret_cast<const char*>(a.v) + at), v_off[n], to_lds + L::TILE);
+      const int key = (n * L::WAVES + wave) * L::RPI;  // a load's keys lie in one page
+      const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(w.hi, key))) << 32 |
+                          static_cast<uint32_t>(__builtin_amdgcn_readlane(w.lo, key));
+      dma16(reinterpret_cast<const char*>(cache) + at, off[n], to_lds + key * ROW);
     }
   };
 
-  v16f o[DT];
+  const int kx = L::k_place(l32, half) * 16;                    // XOR a step's 32 bytes: the lane's chunk of its key
+  const int vkey = 4 * half + (lane >> 2 & 3);                  // the lane's key of a transposing read, of 8
+  uint32_t k_read[DS], v_read[DT];
+#pragma unroll
+  for (int c = 0; c < DS; ++c) k_read[c] = lds + l32 * ROW + (kx ^ c * 32);
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+    v_read[d] = lds + 2 * L::TILE + vkey * ROW + (lane >> 4 & 1) * 32 + (lane & 3) * 8 + (d ^ L::v_turn(lane >> 2 & 3)) * 64;
+
+  v16f o[DT], s[KT];
+  v8bf w[KT][2];
 #pragma unroll
   for (int d = 0; d < DT; ++d) o[d] = 0.0f;
   float mx = kNoMax, sum = 0.0f;
-  const int kx = L::k_place(l32, half) * 16;                    // XOR a step's 32 bytes: the lane's chunk of its key
-  const int vkey = 4 * half + (lane >> 2 & 3);                  // the lane's key of a transposing read, of 8
-  const uint32_t k_read = lds + l32 * ROW, v_read = lds + L::TILE + vkey * ROW + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
 
-  PD
-  int ids = 0, next_ids = 0;
-  if (from < to) {
-    ids = pages(from);
-    next_ids = pages(from + 1);
-    load(from, ids);
-  }
-  for (int i = from; i < to; ++i) {
-    const int key0 = key_of(i);
-    const uint64_t none = __ballot(ids < 0 || ids >= a.n_pages);  // lanes of keys whose page is none
-    wait_vm0();
-    lds_barrier();
-    ids = next_ids;
-    if (i + 1 < to) load(i + 1, ids);
-    next_ids = pages(i + 2);
-    if (none != 0 || key0 + KEYS > k.hi || (key0 < k.lo && key0 + KEYS > a.sinks)) {
-      // what no row of the tile sees may hold anything: its weight 0 must meet a number
-      char* v = smem + (i & 1) * 2 * L::TILE + L::TILE;
-      for (int c = threadIdx.x; c < L::TILE / 16; c += 64 * WAVES) {
-        const int key = c / L::CHUNKS, j = key0 + key;
-        if (j >= k.hi || (j < k.lo && j >= a.sinks) || (none >> key & 1)) *reinterpret_cast<v4f*>(v + c * 16) = 0.0f;
-      }
-      lds_barrier();
-    }
-    // blocks that none of the wave's rows sees
-    if (key0 > p_high || (a.window > 0 && key0 >= a.sinks && key0 + KEYS <= p_low - a.window + 1)) continue;
-
-    PA
-    const uint32_t kb = k_read + (i & 1) * 2 * L::TILE, vb = v_read + (i & 1) * 2 * L::TILE;
-    v16f s[KT];
+  // Operand of product n of a block's scores, and of its second product, in buffer `odd`.
+  auto read_k = [&](int odd, int n) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) v8bf*>(k_read[n / KT] + odd * L::TILE + n % KT * 32 * ROW);
+  };
+  auto read_v = [&](int odd, int n) {
+    const uint32_t at = v_read[n % DT] + odd * L::TILE + (n / (2 * DT) * 32 + n / DT % 2 * 16) * ROW;
+    const v4bf lo = read_tr(at), hi = read_tr(at + 8 * ROW);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  // The scores of the block in buffer `odd` and the second product of the one before it, in turn
+  // (their chains of products are apart), operands read AHEAD products before.
+  constexpr int N = DS * KT, AHEAD = 3;
+  auto products = [&](int odd) {
+    v8bf kf[AHEAD], vf[AHEAD];
 #pragma unroll
     for (int x = 0; x < KT; ++x) s[x] = 0.0f;
 #pragma unroll
-    for (int c = 0; c < DS; ++c)
+    for (int n = 0; n < AHEAD; ++n) {
+      kf[n] = read_k(odd, n);
+      vf[n] = read_v(1 - odd, n);
+    }
 #pragma unroll
-      for (int x = 0; x < KT; ++x) {
-        const v8bf kf = *reinterpret_cast<const __attribute__((address_space(3))) v8bf*>(kb + (kx ^ c * 32) + x * 32 * ROW);
-        s[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[c], s[x], 0, 0, 0);
+    for (int n = 0; n < N; ++n) {
+      __builtin_amdgcn_sched_barrier(0);
+      s[n % KT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[n % AHEAD], q[n / KT], s[n % KT], 0, 0, 0);
+      o[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[n % AHEAD], w[n / (2 * DT)][n / DT % 2], o[n % DT], 0, 0, 0);
+      if (n + AHEAD < N) {
+        kf[n % AHEAD] = read_k(odd, n + AHEAD);
+        vf[n % AHEAD] = read_v(1 - odd, n + AHEAD);
       }
-    if (none != 0 || key0 + KEYS - 1 > p_low || key0 + KEYS > t.seen || (a.window > 0 && key0 <= p_high - a.window)) {
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Block i's scores to weights.
+  auto weigh = [&](int i, uint64_t none) {
+    if (none != 0 || i < calm_from || i >= calm_to) {
+      const int key0 = key_of(i);
 #pragma unroll
       for (int x = 0; x < KT; ++x)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int key = x * 32 + 8 * (r >> 2) + 4 * half + (r & 3), j = key0 + key;
-          const bool sees = j <= p && j < t.seen && (a.window == 0 || p - j < a.window || j < a.sinks) && !(none >> key & 1);
-          s[x][r] = sees ? s[x][r] : -__builtin_inff();
+          const bool hidden = (j > p) | (j >= t.seen) | ((a.window > 0) & (p - j >= a.window) & (j >= a.sinks)) | static_cast<bool>(none >> key & 1);
+          s[x][r] = hidden ? -__builtin_inff() : s[x][r];
         }
     }
-    PB
-    float top = s[0][0];
+    float tops[4];  // chains of their own: a dependent operation waits twice as long as the next one
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tops[c] = s[c % KT][c];
 #pragma unroll
     for (int x = 0; x < KT; ++x)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[x][r]);
+      for (int r = 0; r < 16; r += 2) tops[r / 2 % 4] = fmaxf(fmaxf(tops[r / 2 % 4], s[x][r]), s[x][r + 1]);
+    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     top = fmaxf(top, other_half(top)) * scale;
     if (__any(top > mx + 8.0f)) {
       const float now = fmaxf(mx, top), alpha = __builtin_amdgcn_exp2f(mx - now);
@@ -512,7 +531,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_large_
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] *= alpha;
     }
-    v8bf w[KT][2];
+    float sums[2] = {sum, 0.0f};
 #pragma unroll
     for (int x = 0; x < KT; ++x)
 #pragma unroll
@@ -520,21 +539,58 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_large_
         v2bf pair;
         pair[0] = static_cast<__bf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x][r], scale, -mx)));
         pair[1] = static_cast<__bf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x][r + 1], scale, -mx)));
-        sum = add_pair(pair, sum);  // the weights as the product has them
+        sums[r / 2 & 1] = add_pair(pair, sums[r / 2 & 1]);  // the weights as the product has them
         w[x][r >> 3][r & 7] = pair[0];
         w[x][r >> 3][(r & 7) + 1] = pair[1];
       }
-    PC
+    sum = sums[0] + sums[1];
+  };
+  // What no row of the tile sees of block i's values may hold anything: its weight 0 must meet a number.
+  auto clean = [&](int i, int odd, uint64_t none) {
+    if (none == 0 && i >= whole_from && i < whole_to) return;
+    const int key0 = key_of(i);
+    char* v = smem + (2 + odd) * L::TILE;
+    for (int c = threadIdx.x; c < L::TILE / 16; c += 64 * L::WAVES) {
+      const int key = c / L::CHUNKS, j = key0 + key;
+      if (j >= k.hi || (j < k.lo && j >= a.sinks) || (none >> key & 1)) *reinterpret_cast<v4f*>(v + c * 16) = 0.0f;
+    }
+    lds_barrier();
+  };
+
+  if (from < to) {
+    // here: block i's keys, then: block i + 1's, ids: the pages of block i + 2
+    Where here = where(from, pages(from)), then = where(from + 1, pages(from + 1));
+    int ids = pages(from + 2);
+    load(here, a.k, k_off, lds);
+    wait_vm0();
+    bare_barrier();
+    load(then, a.k, k_off, lds + L::TILE);  // the last block once more where there is none
+    load(here, a.v, v_off, lds + 2 * L::TILE);
 #pragma unroll
-    for (int x = 0; x < KT; ++x)
+    for (int x = 0; x < KT; ++x) s[x] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const uint32_t at = vb + (d ^ L::v_turn(lane >> 2 & 3)) * 64 + (x * 32 + e * 16) * ROW;
-          const v4bf lo = read_tr(at), hi = read_tr(at + 8 * ROW);
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), w[x][e], o[d], 0, 0, 0);
-        }
+    for (int n = 0; n < N; ++n) s[n % KT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_k(0, n), q[n / KT], s[n % KT], 0, 0, 0);
+    // Block i, whose buffers are `odd`: its weights, then its second product beside the next one's scores
+    // (of the last, what the buffer holds: they are not used).
+    auto step = [&](int i, int odd) {
+      weigh(i, here.none);
+      wait_vm0();
+      lds_barrier();
+      const uint64_t none = here.none;
+      here = then;
+      then = where(i + 2, ids);
+      ids = pages(i + 3);
+      if (i + 2 < to) load(then, a.k, k_off, lds + odd * L::TILE);
+      if (i + 1 < to) load(here, a.v, v_off, lds + (3 - odd) * L::TILE);
+      clean(i, odd, none);
+      products(1 - odd);
+    };
+    for (int i = from; i < to; i += 2) {
+      step(i, 0);
+      if (i + 1 >= to) break;
+      step(i + 1, 1);
+    }
+    wait_vm0();
   }
 
   sum += other_half(sum);
@@ -627,7 +683,7 @@ constexpr int kSmallMost = 64;
 // sequence's length says which one takes it.
 struct Plan {
   bool small, large;
-  int waves, small_rows, splits, large_splits, max_splits;
+  int small_rows, splits, large_splits, max_splits;
 };
 
 Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_keys, int window, int sinks, const DeviceInfo& dev) {
@@ -639,33 +695,25 @@ Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_k
   // few rows: workgroups that share a tile's keys, enough to fill the device and none of less
   // than kSplitBlocks blocks of what the table can hold
   int64_t keys = table_keys;
-  if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + kSmallRows + 2 * kSmallKeys);
+  if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + 256);
   const int64_t most = std::max<int64_t>(1, (keys + kSmallKeys - 1) / kSmallKeys / kSplitBlocks);
   const int64_t tiles = std::max<int64_t>(1, std::min(T, T * group / kSmallRows + std::min(B, T))) * n_kv;
   p.splits = !p.small ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, kMostSplits), (D == 64 ? 12 : D == 128 ? 8 : 4) * dev.cu_count / tiles)));
-  // many rows: 256 a workgroup where that still fills the device, else 128, and splits below that
-  const int64_t rows = T * group * n_kv;
-  p.waves = D < 256 && rows / 256 >= 2 * dev.cu_count ? 8 : 4;
-  const int64_t large_tiles = std::max<int64_t>(1, rows / (32 * p.waves));
-  p.large_splits = !p.large ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(table_keys / 512, 16), dev.cu_count / large_tiles)));
+  // many rows: two workgroups of 128 a CU (one for D = 256), or that many splits of fewer
+  const int64_t large_tiles = std::max<int64_t>(1, T * group * n_kv / 128), slots = (D < 256 ? 2 : 1) * dev.cu_count;
+  p.large_splits = !p.large ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(keys / 512, 16), slots / large_tiles)));
   p.max_splits = std::max(p.splits, p.large_splits);
   return p;
 }
 
-template <int D, int WAVES>
-hipError_t launch_large(AttnArgs& a, hipStream_t stream) {
-  using L = Large<D, WAVES>;
-  a.large_rows = L::ROWS;
-  a.large_keys = L::KEYS;
-  attention_large_kernel<D, WAVES><<<static_cast<uint32_t>(tiles_of(a, L::ROWS)) * a.n_kv * a.large_splits, 64 * WAVES, 0, stream>>>(a);
-  return hipGetLastError();
-}
-
 template <int D>
 hipError_t launch_d(AttnArgs a, const Plan& p, hipStream_t stream) {
-  a.large_rows = a.large_keys = 32;
+  using L = Large<D>;
+  a.large_rows = L::ROWS;
+  a.large_keys = L::KEYS;
   if (p.large) {
-    const hipError_t e = p.waves == 8 && D < 256 ? launch_large<D, D < 256 ? 8 : 4>(a, stream) : launch_large<D, 4>(a, stream);
+    attention_large_kernel<D><<<static_cast<uint32_t>(tiles_of(a, L::ROWS)) * a.n_kv * a.large_splits, 64 * L::WAVES, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const uint32_t tiles = static_cast<uint32_t>(tiles_of(a, kSmallRows)) * a.n_kv;

@@ -456,11 +456,13 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
 
   const int kx = L::k_place(l32, half) * 16;                    // XOR a step's 32 bytes: the lane's chunk of its key
   const int vkey = 4 * half + (lane >> 2 & 3);                  // the lane's key of a transposing read, of 8
-  uint32_t k_read[DS], v_read[DT];
+  // (the swizzles turn over 256 bytes: what lies 256 on has the same address but for that)
+  constexpr int KR = DS < 8 ? DS : 8, VR = DT < 4 ? DT : 4;
+  uint32_t k_read[KR], v_read[VR];
 #pragma unroll
-  for (int c = 0; c < DS; ++c) k_read[c] = lds + l32 * ROW + (kx ^ c * 32);
+  for (int c = 0; c < KR; ++c) k_read[c] = lds + l32 * ROW + (kx ^ c * 32);
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+  for (int d = 0; d < VR; ++d)
     v_read[d] = lds + 2 * L::TILE + vkey * ROW + (lane >> 4 & 1) * 32 + (lane & 3) * 8 + (d ^ L::v_turn(lane >> 2 & 3)) * 64;
 
   v16f o[DT], s[KT];
@@ -471,16 +473,16 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
 
   // Operand of product n of a block's scores, and of its second product, in buffer `odd`.
   auto read_k = [&](int odd, int n) {
-    return *reinterpret_cast<const __attribute__((address_space(3))) v8bf*>(k_read[n / KT] + odd * L::TILE + n % KT * 32 * ROW);
+    return *reinterpret_cast<const __attribute__((address_space(3))) v8bf*>(k_read[n / KT % KR] + odd * L::TILE + n / KT / KR * 256 + n % KT * 32 * ROW);
   };
   auto read_v = [&](int odd, int n) {
-    const uint32_t at = v_read[n % DT] + odd * L::TILE + (n / (2 * DT) * 32 + n / DT % 2 * 16) * ROW;
+    const uint32_t at = v_read[n % DT % VR] + n % DT / VR * 256 + odd * L::TILE + (n / (2 * DT) * 32 + n / DT % 2 * 16) * ROW;
     const v4bf lo = read_tr(at), hi = read_tr(at + 8 * ROW);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
   // The scores of the block in buffer `odd` and the second product of the one before it, in turn
   // (their chains of products are apart), operands read AHEAD products before.
-  constexpr int N = DS * KT, AHEAD = 3;
+  constexpr int N = DS * KT, AHEAD = 2;
   auto products = [&](int odd) {
     v8bf kf[AHEAD], vf[AHEAD];
 #pragma unroll

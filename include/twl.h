@@ -474,7 +474,8 @@ size_t twl_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   q         out: bf16 [M, n_q, D]
  *   k_cache, v_cache out: bf16 [n_pages, n_kv, page, D]; slots of no token keep theirs
  * D is 64, 128 or 256; n_q a multiple of n_kv of at most TWL_MAX_HEADS; rot a multiple
- * of 16 up to D; page a power of two from 1 to 1024, at most 2^31 - 1 slots.  Outputs that
+ * of 16 up to D; eps at least 2^-126; page a power of two from 1 to 1024, at most 2^31 - 1
+ * slots.  Outputs that
  * overlap an input or each other are TWL_EINVAL.  A value that is not finite reaches its
  * own head only.  Sums of squares beyond fp32's range give unspecified results.
  */

@@ -4,6 +4,7 @@
 #include "api_common.h"
 #include "attention_internal.h"
 
+#include <cfloat>
 #include <cmath>
 
 namespace {
@@ -129,7 +130,8 @@ twl_status twl_qk_norm_rope(const void* qkv, int kind, int64_t row_stride, const
   if (row_stride < width || row_stride % 8 != 0 || row_stride > (int64_t{1} << 30))
     return fail(TWL_ESHAPE, "row_stride=%lld must be a multiple of 8 from %lld to 2^30", static_cast<long long>(row_stride),
                 static_cast<long long>(width));
-  if (!(eps > 0.0) || !std::isfinite(eps)) return fail(TWL_EINVAL, "eps=%g must be positive and finite", eps);
+  if (!(static_cast<float>(eps) >= FLT_MIN) || !std::isfinite(static_cast<float>(eps)))
+    return fail(TWL_EINVAL, "eps=%g must be at least 2^-126 and finite as fp32", eps);
   if (rot < 0 || rot > D || rot % 16 != 0)
     return fail(TWL_ESHAPE, "rot=%lld must be a multiple of 16 of at most %lld", static_cast<long long>(rot), static_cast<long long>(D));
   TWL_TRY(check_rows("n_pos", n_pos));

@@ -116,7 +116,7 @@ __device__ __forceinline__ Blocks find_blocks(const AttnArgs& a, const Tile& t, 
 
 // Splits of a tile's blocks that do work: at most a.splits, each of kSplitBlocks or more.
 constexpr int kSmallRows = 16, kSmallKeys = 32, kSmallWaves = 4, kSplitBlocks = 2 * kSmallWaves;
-constexpr int kLargeSplitBlocks = 4;
+constexpr int kLargeSplitBlocks = 2;
 
 __device__ __forceinline__ int large_splits(const AttnArgs& a, int total) {
   return max(1, min(a.large_splits, total / kLargeSplitBlocks));
@@ -618,18 +618,20 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
   }
 }
 
-// The splits of a row joined: a workgroup a row, eight splits a wave, so that one wait (2 us for
-// sums that another XCD wrote) covers them all.  A wave a row with eight splits at a time took
-// 17 us for 64 splits, this 4; more than 32 splits were no faster (32768 keys: 34.9 us of 64, 34.1 of 32).
+// The splits of a row joined, eight splits a wave, so that one wait (2 us for sums that another XCD
+// wrote) covers them all: a wave a row for up to eight splits (WAVES = 1; the calls with many rows),
+// else a workgroup of four waves.  One wave for all splits, eight at a time, took 17 us for 64 of
+// them, this 4; more than 32 splits were no faster (32768 keys: 34.9 us with 64, 34.1 with 32).
 constexpr int kMostSplits = 32;
 
-template <int D>
+template <int D, int WAVES>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   constexpr int PER = D / 64;
   typedef std::conditional_t<PER == 1, float, float __attribute__((ext_vector_type(PER == 1 ? 2 : PER)))> vec;
   __shared__ vec joined[4][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t rows = static_cast<int64_t>(a.T) * a.n_q, out_row = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave_id % WAVES;
+  const int64_t rows = static_cast<int64_t>(a.T) * a.n_q, out_row = static_cast<int64_t>(blockIdx.x) * (4 / WAVES) + wave_id / WAVES;
+  if (out_row >= rows) return;
   // lane s: maximum and sum of split s; and the sums of the wave's first splits: loaded before it is
   // known how many there are, which the lengths say (what was not written is not used)
   const float* ml = a.part + a.max_splits * rows * D + (min(lane, a.max_splits - 1) * rows + out_row) * 2;
@@ -637,7 +639,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   const float* part = a.part + out_row * D + lane * PER;
   vec v[8];
 #pragma unroll
-  for (int s = 0; s < 8; ++s) v[s] = *reinterpret_cast<const vec*>(part + min(wave * 8 + s, a.max_splits - 1) * rows * D);
+  for (int s = 0; s < 8; ++s) v[s] = wave * 8 + s < a.max_splits ? *reinterpret_cast<const vec*>(part + (wave * 8 + s) * rows * D) : vec(0.0f);
   Tile t;
   const int token = static_cast<int>(out_row / a.n_q), qh = static_cast<int>(out_row % a.n_q);
   if (!find_sequence(a, lane, &t, [&](int q0, int) { return q0 <= token; }) || token >= t.q0 + t.n) return;
@@ -663,10 +665,13 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 #pragma unroll
   for (int s = 0; s < 8; ++s)
     if (wave * 8 + s < splits) acc += v[s] * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), wave * 8 + s));
-  joined[wave][lane] = acc;
-  __syncthreads();
-  if (wave != 0) return;
-  acc = (joined[0][lane] + joined[1][lane] + joined[2][lane] + joined[3][lane]) * (all > 0.0f ? 1.0f / all : 0.0f);
+  if constexpr (WAVES > 1) {
+    joined[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+    acc = joined[0][lane] + joined[1][lane] + joined[2][lane] + joined[3][lane];
+  }
+  acc *= all > 0.0f ? 1.0f / all : 0.0f;
   if constexpr (PER == 1) {
     *reinterpret_cast<__bf16*>(a.out + out_row * D + lane) = static_cast<__bf16>(acc);
   } else {
@@ -690,20 +695,40 @@ struct Plan {
 
 Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_keys, int window, int sinks, const DeviceInfo& dev) {
   Plan p = {};
-  const bool few = T * group <= kSmallMost * B || T * group <= kSmallMost;
+  int64_t keys = table_keys;  // of a tile, at most
+  if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + 256);
+  // Few rows: workgroups that share a tile's keys, enough to fill the device (several times over, for lengths
+  // that differ: 24 tokens of up to 16384 keys of 256 took 227 us with one workgroup a CU, 203 with two, 188 with
+  // four, 199 with eight) and none of less than kSplitBlocks blocks of what the table can hold.
+  const int64_t tiles = std::max<int64_t>(1, std::min(T, T * group / kSmallRows + std::min(B, T))) * n_kv;
+  const int64_t most = std::min<int64_t>(std::max<int64_t>(1, (keys + kSmallKeys - 1) / kSmallKeys / kSplitBlocks), kMostSplits);
+  p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (D == 64 ? 12 : D == 128 ? 8 : 4) * dev.cu_count / tiles)));
+  // Many rows: where the tiles leave workgroups' places free (two a CU, one for D = 256), splits, if what
+  // they save (a block of keys takes 1.7 us where few workgroups run) is more than the second
+  // kernel and the sums' way through memory (4 TB/s).  us with the splits chosen and without: 512 of 16384 keys
+  // 185 and 387, 2 x 924 tokens of 4 heads 25 and 33; 512 tokens of 40 heads 22 without, 33 with 3.
+  const int64_t large_tiles = std::max<int64_t>(1, T * group * n_kv / 128), places = (D < 256 ? 2 : 1) * dev.cu_count;
+  const int64_t blocks = (keys + (D < 256 ? 63 : 31)) / (D < 256 ? 64 : 32);
+  float large_us = 0.0f;
+  for (int64_t n = 1; n == 1 || (n <= std::min<int64_t>(kMostSplits, blocks / kLargeSplitBlocks) && n * large_tiles <= places); ++n) {
+    float us = 1.7f * static_cast<float>((blocks + n - 1) / n) * static_cast<float>((n * large_tiles + places - 1) / places);
+    if (n > 1) us += 4.0f + static_cast<float>(n * T) * static_cast<float>(n_kv * group * (D + 2)) * 8.0f / 4e6f;
+    if (n > 1 && us >= large_us) continue;
+    large_us = us;
+    p.large_splits = static_cast<int>(n);
+  }
+  // Which of the two: the kernel for few rows reads a tile's keys for 16 rows instead of 128 (25000 keys a us
+  // for all tiles of D = 128), but has its keys shared by four waves and needs no second launch in a batch.
+  // us, few and many: 2 x 28 tokens of 56 keys of 256 10.5 and 20, 10 x 111 of 223 10.3 and 20; 200 tokens of 4000
+  // keys 86 and 43.  A round of workgroups that waits for places (four a CU, two, one by D) adds 4 us.
+  const float small_us = std::max(static_cast<float>(tiles * keys) * static_cast<float>(D) / 128.0f / 25000.0f, static_cast<float>(keys) * 0.01f / static_cast<float>(p.splits)) +
+                         (p.splits > 1 ? 4.0f : 0.0f) + 4.0f * static_cast<float>(tiles * p.splits / ((D == 64 ? 4 : D == 128 ? 2 : 1) * dev.cu_count));
+  const bool few = T * group <= kSmallMost * B || small_us < large_us + (B > 1 ? 4.0f : 0.0f);
   p.small = few || B > 1;
   p.large = !few;
   p.small_rows = few ? 1 << 30 : B == 1 ? 0 : kSmallMost;
-  // few rows: workgroups that share a tile's keys, enough to fill the device and none of less
-  // than kSplitBlocks blocks of what the table can hold
-  int64_t keys = table_keys;
-  if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + 256);
-  const int64_t most = std::max<int64_t>(1, (keys + kSmallKeys - 1) / kSmallKeys / kSplitBlocks);
-  const int64_t tiles = std::max<int64_t>(1, std::min(T, T * group / kSmallRows + std::min(B, T))) * n_kv;
-  p.splits = !p.small ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, kMostSplits), (D == 64 ? 12 : D == 128 ? 8 : 4) * dev.cu_count / tiles)));
-  // many rows: two workgroups of 128 a CU (one for D = 256), or that many splits of fewer
-  const int64_t large_tiles = std::max<int64_t>(1, T * group * n_kv / 128), slots = (D < 256 ? 2 : 1) * dev.cu_count;
-  p.large_splits = !p.large ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(keys / 512, 16), slots / large_tiles)));
+  if (!p.small) p.splits = 1;
+  if (!p.large) p.large_splits = 1;
   p.max_splits = std::max(p.splits, p.large_splits);
   return p;
 }
@@ -725,7 +750,11 @@ hipError_t launch_d(AttnArgs a, const Plan& p, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   if (a.max_splits == 1) return hipSuccess;
-  attention_join_kernel<D><<<static_cast<uint32_t>(a.T * a.n_q), 256, 0, stream>>>(a);
+  const uint32_t rows = static_cast<uint32_t>(a.T) * a.n_q;
+  if (a.max_splits <= 8)
+    attention_join_kernel<D, 1><<<(rows + 3) / 4, 256, 0, stream>>>(a);
+  else
+    attention_join_kernel<D, 4><<<rows, 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -474,10 +474,10 @@ size_t twl_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   q         out: bf16 [M, n_q, D]
  *   k_cache, v_cache out: bf16 [n_pages, n_kv, page, D]; slots of no token keep theirs
  * D is 64, 128 or 256; n_q a multiple of n_kv of at most TWL_MAX_HEADS; rot a multiple
- * of 16 up to D; eps at least 2^-126; page a power of two from 1 to 1024, at most 2^31 - 1
- * slots.  Outputs that
- * overlap an input or each other are TWL_EINVAL.  A value that is not finite reaches its
- * own head only.  Sums of squares beyond fp32's range give unspecified results.
+ * of 16 up to D; eps at least 2^-126; page a power of two from 1 to 1024, at most
+ * 2^31 - 1 slots.  Outputs that overlap an input or each other are TWL_EINVAL.  A value
+ * that is not finite reaches its own head only.  Sums of squares beyond fp32's range give
+ * unspecified results.
  */
 #define TWL_MAX_HEADS 1024
 twl_status twl_qk_norm_rope(const void* qkv, int kind, int64_t row_stride, const uint16_t* q_weight,
@@ -505,18 +505,19 @@ twl_status twl_qk_norm_rope(const void* qkv, int kind, int64_t row_stride, const
  *   q_start    in : int32 [B + 1], from 0, not decreasing; rows of q from q_start[B] on
  *                   have no sequence: their out is left as it was.  Starts outside
  *                   0 .. T are taken as the nearest of the two.
- *   kv_len     in : int32 [B] (below 0: 0)
+ *   kv_len     in : int32 [B] (below 0: 0; above 2^30: 2^30)
  *   out        out: bf16 [T, n_q, D]
  *   workspace     : twl_attention_workspace_bytes of the same sizes, contents on entry do
  *                   not matter; calls sharing one must not run concurrently
  * D is 64, 128 or 256; n_q a multiple of n_kv of at most TWL_MAX_HEADS; page a power of
  * two from 16 to 1024; window and sinks 0 to 2^30 (sinks matter with a window only);
- * T n_q up to 2^27, B n_kv up to 2^22.  The lengths are read on the device only, so that a
- * captured call serves other lengths of the same T, B and table.  Keys and values that
- * no row of a sequence sees may hold anything; values that are not finite in one that
- * some row sees may reach the sequence's other rows.  An output or workspace that overlaps
- * an input is TWL_EINVAL.
+ * T n_q up to 2^27, B up to TWL_MAX_SEQUENCES, B n_kv up to 2^22, table_pages page up
+ * to 2^30.  The lengths are read on the device only, so that a captured call serves other
+ * lengths of the same T, B and table.  Keys and values that no row of a sequence sees may
+ * hold anything; values that are not finite in one that some row sees may reach the
+ * sequence's other rows.  An output or workspace that overlaps an input is TWL_EINVAL.
  */
+#define TWL_MAX_SEQUENCES 65536
 twl_status twl_window_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache,
                                 const int32_t* page_table, const int32_t* q_start, const int32_t* kv_len, double scale,
                                 int64_t window, int64_t sinks, int64_t T, int64_t B, int64_t n_q, int64_t n_kv,

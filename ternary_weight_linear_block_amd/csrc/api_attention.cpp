@@ -55,9 +55,12 @@ twl_status check_attention(int64_t T, int64_t B, int64_t n_q, int64_t n_kv, int6
   TWL_TRY(check_pages(0, page, 16, n_kv, D));
   TWL_TRY(check_rows("window", window));
   TWL_TRY(check_rows("sinks", sinks));
-  if (T * n_q > (int64_t{1} << 27) || B * n_kv > (int64_t{1} << 22))
-    return fail(TWL_ESHAPE, "T=%lld, B=%lld: at most 2^27 rows T n_q and 2^22 of B n_kv", static_cast<long long>(T),
-                static_cast<long long>(B));
+  if (T * n_q > (int64_t{1} << 27) || B > TWL_MAX_SEQUENCES || B * n_kv > (int64_t{1} << 22))
+    return fail(TWL_ESHAPE, "T=%lld, B=%lld: at most 2^27 rows T n_q, %d sequences and 2^22 of B n_kv", static_cast<long long>(T),
+                static_cast<long long>(B), TWL_MAX_SEQUENCES);
+  if (table_pages * page > (int64_t{1} << 30))
+    return fail(TWL_ESHAPE, "table_pages=%lld of %lld tokens: at most 2^30 tokens", static_cast<long long>(table_pages),
+                static_cast<long long>(page));
   return TWL_OK;
 }
 

@@ -22,20 +22,16 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 
-// Start of a running maximum: finite, so that differences of two of them are numbers;
-// a masked score is -infinity and its weight exactly 0.
-constexpr float kNoMax = -1e30f;
+// Start of a running maximum: finite, so that differences of two of them are numbers, and
+// below every score; a masked score is -infinity and its weight exactly 0.
+constexpr float kNoMax = -3.4028235e38f;
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char*)(p)));
 }
 
-// Direct global->LDS load of 16 bytes a lane to lds_base + 16 * lane (see gemm_i8.hip).
-__device__ __forceinline__ void dma16(const void* src, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_base) : "memory", "m0");
-}
-
-// The same from a wave-uniform address plus a lane's offset.
+// Direct global->LDS load of 16 bytes a lane, from a wave-uniform address plus a lane's offset to
+// lds_base + 16 * lane (see gemm_i8.hip).
 __device__ __forceinline__ void dma16(const void* base, uint32_t offset, uint32_t lds_base) {
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds_base) : "memory", "m0");
 }
@@ -54,6 +50,9 @@ __device__ __forceinline__ v4bf read_tr(uint32_t addr) {
   return __builtin_bit_cast(v4bf, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                       reinterpret_cast<__attribute__((address_space(3))) v4s*>(addr)));
 }
+
+// Longest context (a table holds no more): positions, windows and their sums stay within 32 bits.
+constexpr int kMostKeys = 1 << 30;
 
 // One sequence's share of a workgroup's tile of `rows` packed rows (a row: a new token
 // and one of the g query heads of a key head, row = token * g + head).
@@ -79,7 +78,7 @@ __device__ __forceinline__ bool find_sequence(const AttnArgs& a, int lane, Tile*
       t->seq = base + here - 1;
       t->q0 = __builtin_amdgcn_readlane(q0, here - 1);
       t->n = min(max(__builtin_amdgcn_readlane(end, here - 1), t->q0), a.T) - t->q0;
-      t->kv = max(__builtin_amdgcn_readlane(kv, here - 1), 0);
+      t->kv = min(max(__builtin_amdgcn_readlane(kv, here - 1), 0), kMostKeys);
     }
     if (here < 64) break;
   }
@@ -88,12 +87,13 @@ __device__ __forceinline__ bool find_sequence(const AttnArgs& a, int lane, Tile*
 }
 
 // The sequence of tile `tile`: sequence b owns the tiles from floor(q_start[b] g / rows) + b,
-// which leaves it at least ceil(n g / rows) of them.  False for a tile without rows.
+// which leaves it at least ceil(n g / rows) of them.  False for a tile without rows (and, where
+// starts decrease, for one before its sequence).
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, int rows, int lane, Tile* t) {
   auto first = [&](int q0, int b) { return static_cast<int>(static_cast<int64_t>(q0) * a.group / rows) + b; };
   if (!find_sequence(a, lane, t, [&](int q0, int b) { return first(q0, b) <= tile; })) return false;
   t->row0 = (tile - first(t->q0, t->seq)) * rows;
-  return t->row0 < t->n * a.group;
+  return t->row0 >= 0 && t->row0 < t->n * a.group;
 }
 
 // The blocks of `size` keys that the rows of a tile see: `sink` blocks from key 0 and
@@ -469,7 +469,7 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
   v8bf w[KT][2];
 #pragma unroll
   for (int d = 0; d < DT; ++d) o[d] = 0.0f;
-  float mx = kNoMax, sum = 0.0f;
+  float mx = scale > 1.0f ? kNoMax / scale : kNoMax, sum = 0.0f;  // the maximum, not scaled yet
 
   // Operand of product n of a block's scores, and of its second product, in buffer `odd`.
   auto read_k = [&](int odd, int n) {
@@ -525,13 +525,25 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
 #pragma unroll
       for (int r = 0; r < 16; r += 2) tops[r / 2 % 4] = fmaxf(fmaxf(tops[r / 2 % 4], s[x][r]), s[x][r + 1]);
     float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    top = fmaxf(top, other_half(top)) * scale;
-    if (__any(top > mx + 8.0f)) {
-      const float now = fmaxf(mx, top), alpha = __builtin_amdgcn_exp2f(mx - now);
+    top = fmaxf(top, other_half(top));
+    // s scale - mx scale in one operation: exact but for the rounding of mx scale, a factor of all of a row's
+    // weights that divides out, and is at most 2^2 up to 2^26; beyond it the difference comes first
+    float factor = scale, shift = mx * scale;
+    if (__any(((top - mx) * scale > 8.0f) | (__builtin_fabsf(shift) > 0x1p26f))) {
+      const float now = fmaxf(mx, top), alpha = __builtin_amdgcn_exp2f((mx - now) * scale);
       mx = now;
+      shift = mx * scale;
       sum *= alpha;
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] *= alpha;
+      if (__any(__builtin_fabsf(shift) > 0x1p26f)) {
+#pragma unroll
+        for (int x = 0; x < KT; ++x)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[x][r] = (s[x][r] - mx) * scale;
+        factor = 1.0f;
+        shift = 0.0f;
+      }
     }
     float sums[2] = {sum, 0.0f};
 #pragma unroll
@@ -539,8 +551,8 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
 #pragma unroll
       for (int r = 0; r < 16; r += 2) {
         v2bf pair;
-        pair[0] = static_cast<__bf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x][r], scale, -mx)));
-        pair[1] = static_cast<__bf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x][r + 1], scale, -mx)));
+        pair[0] = static_cast<__bf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x][r], factor, -shift)));
+        pair[1] = static_cast<__bf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x][r + 1], factor, -shift)));
         sums[r / 2 & 1] = add_pair(pair, sums[r / 2 & 1]);  // the weights as the product has them
         w[x][r >> 3][r & 7] = pair[0];
         w[x][r >> 3][(r & 7) + 1] = pair[1];
@@ -613,7 +625,7 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
     }
   if (!whole && half == 0) {
     float* ml = a.part + static_cast<int64_t>(a.max_splits) * a.T * a.n_q * D + (static_cast<int64_t>(split) * a.T * a.n_q + out_row) * 2;
-    ml[0] = mx;
+    ml[0] = mx * scale;
     ml[1] = sum;
   }
 }
@@ -695,20 +707,25 @@ struct Plan {
 
 Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_keys, int window, int sinks, const DeviceInfo& dev) {
   Plan p = {};
-  int64_t keys = table_keys;  // of a tile, at most
-  if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + 256);
+  // Keys of a tile, at most: whole blocks of what its tokens (rows / group and one more) see.
+  auto reach = [&](int rows, int size) {
+    const int64_t keys = window == 0 ? table_keys : std::min<int64_t>(table_keys, static_cast<int64_t>(window) + sinks + rows / group + 1 + 2 * size);
+    return (keys + size - 1) / size * size;
+  };
+  const int64_t keys = reach(kSmallRows, kSmallKeys), large_size = D < 256 ? 64 : 32;
   // Few rows: workgroups that share a tile's keys, enough to fill the device (several times over, for lengths
   // that differ: 24 tokens of up to 16384 keys of 256 took 227 us with one workgroup a CU, 203 with two, 188 with
   // four, 199 with eight) and none of less than kSplitBlocks blocks of what the table can hold.
   const int64_t tiles = std::max<int64_t>(1, std::min(T, T * group / kSmallRows + std::min(B, T))) * n_kv;
-  const int64_t most = std::min<int64_t>(std::max<int64_t>(1, (keys + kSmallKeys - 1) / kSmallKeys / kSplitBlocks), kMostSplits);
+  const int64_t most = std::min<int64_t>(std::max<int64_t>(1, keys / kSmallKeys / kSplitBlocks),
+                                         std::min<int64_t>(kMostSplits, (1 << 23) / (B * n_kv)));  // the grid stays below 2^24 workgroups
   p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (D == 64 ? 12 : D == 128 ? 8 : 4) * dev.cu_count / tiles)));
   // Many rows: where the tiles leave workgroups' places free (two a CU, one for D = 256), splits, if what
   // they save (a block of keys takes 1.7 us where few workgroups run) is more than the second
   // kernel and the sums' way through memory (4 TB/s).  us with the splits chosen and without: 512 of 16384 keys
   // 185 and 387, 2 x 924 tokens of 4 heads 25 and 33; 512 tokens of 40 heads 22 without, 33 with 3.
   const int64_t large_tiles = std::max<int64_t>(1, T * group * n_kv / 128), places = (D < 256 ? 2 : 1) * dev.cu_count;
-  const int64_t blocks = (keys + (D < 256 ? 63 : 31)) / (D < 256 ? 64 : 32);
+  const int64_t blocks = reach(128, static_cast<int>(large_size)) / large_size;
   float large_us = 0.0f;
   for (int64_t n = 1; n == 1 || (n <= std::min<int64_t>(kMostSplits, blocks / kLargeSplitBlocks) && n * large_tiles <= places); ++n) {
     float us = 1.7f * static_cast<float>((blocks + n - 1) / n) * static_cast<float>((n * large_tiles + places - 1) / places);

@@ -202,6 +202,71 @@ def test_other_scales_and_large_scores(twl, lengths):
     _check(c, _run(twl, c))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lengths", [[(1, 300)] * 4, [(1, 4000)], [(260, 260)], [(200, 3000)]], ids=str)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_near_the_largest(twl, lengths, D, sign):
+    """Scores of about 2^113 with room for fp32's sums: equal ones weigh alike, and of two sizes the larger takes all."""
+    c = _case(17, lengths, 4, 2, D, 16)
+    k_nan = c["k_cache"].isnan()
+    c["q"].fill_(2.0 ** 55)
+    c["k_cache"] = torch.where(k_nan, c["k_cache"], torch.full_like(c["k_cache"], sign * 2.0 ** 55))
+    got = _run(twl, c)
+    equal = _run(twl, dict(c, q=torch.zeros_like(c["q"])))  # all scores 0
+    assert torch.equal(got, equal)
+    _check(dict(c, q=torch.zeros_like(c["q"])), got)
+    top = torch.where(torch.arange(16, device="cuda")[None, None, :, None] == 0, c["k_cache"] * (1.0 + 0.25 * sign), c["k_cache"])
+    got = _run(twl, dict(c, k_cache=top))  # each page's first key wins
+    zero_one = torch.where(k_nan, c["k_cache"], torch.where(torch.arange(16, device="cuda")[None, None, :, None] == 0, 6.0, 0.0).bfloat16())
+    _check(dict(c, q=torch.full_like(c["q"], 6.0), k_cache=zero_one), got)
+
+
+@pytest.mark.parametrize("n", [1, 3, 150])
+def test_lengths_beyond_the_table(twl, n):
+    """What the table does not hold is not seen, at positions up to 2^30 (longer lengths count as that)."""
+    c = _case(18, [(n, 512), (1, 100)], 4, 2, 64, 16)
+    c["kv_len"] = dev(np.array([512 + n, 100], np.int32))  # every new token behind the table
+    want = _run(twl, c)
+    _check(c, want)
+    for kv in (100000, 2 ** 30, 2 ** 30 + 5, 2 ** 31 - 1):
+        c["kv_len"] = dev(np.array([kv, 100], np.int32))
+        assert torch.equal(_run(twl, c), want)
+    got = _run(twl, c, window=2 ** 30, sinks=7)
+    assert torch.equal(got[n:], want[n:])
+    sinks = _run(twl, c, window=50, sinks=7)
+    c["kv_len"] = dev(np.array([512 + n + 50, 100], np.int32))
+    want = _run(twl, c, window=50, sinks=7)
+    _check(c, want, window=50, sinks=7)
+    assert torch.equal(sinks, want)
+    assert (_run(twl, c, window=1)[:n] == 0).all()
+
+
+@pytest.mark.parametrize("n_q,n_kv", [(4, 2), (40, 1)])
+def test_starts_that_decrease_stay_in_bounds(twl, n_q, n_kv):
+    c = _case(19, [(3, 30), (60, 60), (2, 9), (100, 200), (1, 5)], n_q, n_kv, 64, 16, spare_rows=20)
+    T = c["q"].shape[0]
+    guard = torch.full((T + 64, n_q, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    for starts in ([0, 100, 5, 80, 2, 166], [166, 0, 166, 0, 166, 0], [50, 40, 30, 20, 10, 0], [0, 0, 2 ** 31 - 1, -2 ** 31, 63, 64]):
+        c["q_start"] = dev(np.array(starts, np.int32))
+        _run(twl, c, out=guard[32:32 + T])
+        assert (guard[:32] == 7).all() and (guard[32 + T:] == 7).all()
+
+
+def test_most_sequences(twl):
+    c = _case(20, [(1, 40), (2, 2100), (1, 7)], 2, 1, 64, 16)
+    want = _run(twl, c)
+    _check(c, want)
+    for B in (4096, 65536):
+        starts, lens = np.zeros(B + 1, np.int32), np.zeros(B, np.int32)
+        table = np.full((B, c["page_table"].shape[1]), -1, np.int32)
+        at = [5, B // 2, B - 3]
+        for i, (b, n) in enumerate(zip(at, (1, 2, 1))):
+            starts[b + 1:] += n
+            lens[b], table[b] = int(c["kv_len"][i]), host(c["page_table"])[i]
+        many = dict(c, q_start=dev(starts), kv_len=dev(lens), page_table=dev(table))
+        _check(c, _run(twl, many))  # the same rows and keys
+
+
 @pytest.mark.parametrize("n", [1, 200])
 def test_values_not_finite_of_one_sequence_stay_there(twl, n):
     c = _case(10, [(n, 300), (n, 400)], 4, 2, 128, 16)

@@ -140,10 +140,14 @@ __device__ __forceinline__ const void* sgpr_ptr(const void* p) {
   return reinterpret_cast<const void*>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
-// The value of the lane 32 on (or back).
-__device__ __forceinline__ float other_half(float v) {
+// The larger, and the sum, of a lane's value and that of the lane 32 on (or back).
+__device__ __forceinline__ float max_halves(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(threadIdx.x & 32 ? r[0] : r[1]);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 __device__ __forceinline__ float add_pair(v2bf pair, float sum) {
@@ -350,8 +354,7 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
 }
 
 // Many rows: a tile of 128 packed rows a workgroup, 32 of them a wave, whose waves share
-// each block of KT x 32 keys in LDS (two buffers, loaded a block ahead).  Two workgroups share a CU
-// (one for D = 256), so that one has its products while the other has its exponentials.
+// each block of 64 keys in LDS (two buffers, loaded a block ahead).
 //
 // S^T = K Q^T and O^T = V^T P^T on 32x32x16 MFMAs: a lane holds one row (lane % 32) in both,
 // so that maximum, sum and factors are a lane's own (and its partner's, 32 lanes on), and
@@ -361,10 +364,17 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
 //
 // The maximum that weights refer to follows the scores' only when a row's grows by more than
 // 2^8 (weights stay below 2^8, sums far below fp32's range): most blocks leave O as it is.
+//
+// Bound by the MFMAs and, in the shadow of which they must lie, a block's exponentials and maxima.  Heads
+// of 64 and 128: two or three workgroups share a CU, so that one has its products while another has its
+// exponentials; 8192 tokens of 40 heads of 128, window 4096: 510 us, 1010 TFLOP/s (the library's product of
+// 8192^3 in bf16: 1399).  Heads of 256 (O takes 128 registers): one, with all of it between a wave's own
+// products; 4096 causal tokens of 20 heads 210 us, 820 TFLOP/s (one after the other: 243).  What a tile costs
+// beside its blocks, 12 us with two on a CU and 17 alone, is a chain of waits: its sequence, pages, first keys, stores.
 template <int D>
 struct Large {
   static constexpr int WAVES = 4, ROWS = 32 * WAVES;
-  static constexpr int KT = D == 256 ? 1 : 2, KEYS = 32 * KT;
+  static constexpr int KT = 2, KEYS = 32 * KT;                  // tiles of 32 keys of a block
   static constexpr int ROW = 2 * D, CHUNKS = D / 8;             // bytes and 16-byte chunks of a key
   static constexpr int RPI = 1024 / ROW;                        // keys of a load instruction
   static constexpr int LOADS = KEYS / RPI / WAVES;              // load instructions of a wave for K, and for V
@@ -380,6 +390,7 @@ template <int D>
 __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attention_large_kernel(AttnArgs a) {
   using L = Large<D>;
   constexpr int KT = L::KT, KEYS = L::KEYS, ROW = L::ROW, DS = D / 16, DT = D / 32;
+  constexpr bool WIDE = D == 256;
   __shared__ __attribute__((aligned(16))) char smem[4 * L::TILE];  // K of two blocks, V of two
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, half = lane >> 5;
@@ -444,14 +455,15 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
     w.hi = static_cast<uint32_t>(at >> 32);
     return w;
   };
+  auto load_one = [&](const Where& w, const uint16_t* cache, const uint32_t (&off)[L::LOADS], uint32_t to_lds, int n) {
+    const int key = (n * L::WAVES + wave) * L::RPI;  // a load's keys lie in one page
+    const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(w.hi, key))) << 32 |
+                        static_cast<uint32_t>(__builtin_amdgcn_readlane(w.lo, key));
+    dma16(reinterpret_cast<const char*>(cache) + at, off[n], to_lds + key * ROW);
+  };
   auto load = [&](const Where& w, const uint16_t* cache, const uint32_t (&off)[L::LOADS], uint32_t to_lds) {
 #pragma unroll
-    for (int n = 0; n < L::LOADS; ++n) {
-      const int key = (n * L::WAVES + wave) * L::RPI;  // a load's keys lie in one page
-      const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(w.hi, key))) << 32 |
-                          static_cast<uint32_t>(__builtin_amdgcn_readlane(w.lo, key));
-      dma16(reinterpret_cast<const char*>(cache) + at, off[n], to_lds + key * ROW);
-    }
+    for (int n = 0; n < L::LOADS; ++n) load_one(w, cache, off, to_lds, n);
   };
 
   const int kx = L::k_place(l32, half) * 16;                    // XOR a step's 32 bytes: the lane's chunk of its key
@@ -480,9 +492,17 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
     const v4bf lo = read_tr(at), hi = read_tr(at + 8 * ROW);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
+  // O of a wave alone on its SIMD lies in accumulation registers, 128 beside the 200 of all else, which the
+  // compiler does not do by itself (it moved parts of it to and fro, 298 us for 4096 tokens).  It does not
+  // know what the instruction needs either: two states between a weight's last operation and its use, and
+  // `settle` before and behind other operations on O.
+  auto add_values = [&](v16f& acc, v8bf v, v8bf p) {
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(v), "v"(p));
+  };
+  auto settle = [](v16f& acc) { asm volatile("s_nop 15\n\ts_nop 15" : "+a"(acc)); };
   // The scores of the block in buffer `odd` and the second product of the one before it, in turn
   // (their chains of products are apart), operands read AHEAD products before.
-  constexpr int N = DS * KT, AHEAD = 2;
+  constexpr int N = DS * KT, AHEAD = WIDE ? 3 : 2;
   auto products = [&](int odd) {
     v8bf kf[AHEAD], vf[AHEAD];
 #pragma unroll
@@ -504,19 +524,31 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
     }
     __builtin_amdgcn_sched_barrier(0);
   };
+  // The scores of block i that a row does not see become -infinity: the keys that the lane's row sees as
+  // bits, of which an element takes its own (two operations each; the tests for each element took 11).
+  auto mask = [&](v16f (&s)[KT], int i, uint64_t none) {
+    if (none == 0 && i >= calm_from && i < calm_to) return;
+    const int key0 = key_of(i), last = min(p, t.seen - 1) - key0;
+    uint64_t seen = last < 0 ? 0 : ~uint64_t{0} >> (63 - min(last, 63));
+    if (a.window > 0) {
+      const int first = p - a.window + 1 - key0, sinks = a.sinks - key0;
+      const uint64_t near = first > 63 ? 0 : ~uint64_t{0} << max(first, 0), sunk = sinks <= 0 ? 0 : ~uint64_t{0} >> (64 - min(sinks, 64));
+      seen &= near | sunk;
+    }
+    seen = (seen & ~none) >> 4 * half;  // element (x, r) is key x * 32 + 8 (r / 4) + r % 4 behind key0 + 4 half
+#pragma unroll
+    for (int x = 0; x < KT; ++x) {
+      const int bits = static_cast<int>(seen >> x * 32);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const uint32_t keep = __builtin_amdgcn_sbfe(bits, 8 * (r >> 2) + (r & 3), 1);
+        s[x][r] = __uint_as_float((keep & __float_as_uint(s[x][r])) | (~keep & __float_as_uint(-__builtin_inff())));
+      }
+    }
+  };
   // Block i's scores to weights.
   auto weigh = [&](int i, uint64_t none) {
-    if (none != 0 || i < calm_from || i >= calm_to) {
-      const int key0 = key_of(i);
-#pragma unroll
-      for (int x = 0; x < KT; ++x)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int key = x * 32 + 8 * (r >> 2) + 4 * half + (r & 3), j = key0 + key;
-          const bool hidden = (j > p) | (j >= t.seen) | ((a.window > 0) & (p - j >= a.window) & (j >= a.sinks)) | static_cast<bool>(none >> key & 1);
-          s[x][r] = hidden ? -__builtin_inff() : s[x][r];
-        }
-    }
+    mask(s, i, none);
     float tops[4];  // chains of their own: a dependent operation waits twice as long as the next one
 #pragma unroll
     for (int c = 0; c < 4; ++c) tops[c] = s[c % KT][c];
@@ -525,7 +557,7 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
 #pragma unroll
       for (int r = 0; r < 16; r += 2) tops[r / 2 % 4] = fmaxf(fmaxf(tops[r / 2 % 4], s[x][r]), s[x][r + 1]);
     float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    top = fmaxf(top, other_half(top));
+    top = max_halves(top);
     // s scale - mx scale in one operation: exact but for the rounding of mx scale, a factor of all of a row's
     // weights that divides out, and is at most 2^2 up to 2^26; beyond it the difference comes first
     float factor = scale, shift = mx * scale;
@@ -572,59 +604,195 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
   };
 
   if (from < to) {
-    // here: block i's keys, then: block i + 1's, ids: the pages of block i + 2
-    Where here = where(from, pages(from)), then = where(from + 1, pages(from + 1));
-    int ids = pages(from + 2);
-    load(here, a.k, k_off, lds);
-    wait_vm0();
-    bare_barrier();
-    load(then, a.k, k_off, lds + L::TILE);  // the last block once more where there is none
-    load(here, a.v, v_off, lds + 2 * L::TILE);
-#pragma unroll
-    for (int x = 0; x < KT; ++x) s[x] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < N; ++n) s[n % KT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_k(0, n), q[n / KT], s[n % KT], 0, 0, 0);
-    // Block i, whose buffers are `odd`: its weights, then its second product beside the next one's scores
-    // (of the last, what the buffer holds: they are not used).
-    auto step = [&](int i, int odd) {
-      weigh(i, here.none);
+    if constexpr (WIDE) {
+      // One wave a SIMD: a block's weights are formed between the products of the next one's scores and
+      // of the previous one's values, none of which wait for them.
+      // at[x]: block i + x's keys (x = 0, 1, 2), last: the lanes without a page of block i - 1, ids: the pages of block i + 3
+      Where at[3] = {where(from, pages(from)), where(from + 1, pages(from + 1)), where(from + 2, pages(from + 2))};
+      uint64_t last = 0;
+      int ids = pages(from + 3);
+      load(at[0], a.k, k_off, lds);
+      for (int c = threadIdx.x; c < L::TILE / 16; c += 64 * L::WAVES) *reinterpret_cast<v4f*>(smem + 3 * L::TILE + c * 16) = 0.0f;  // no values yet
       wait_vm0();
       lds_barrier();
-      const uint64_t none = here.none;
-      here = then;
-      then = where(i + 2, ids);
-      ids = pages(i + 3);
-      if (i + 2 < to) load(then, a.k, k_off, lds + odd * L::TILE);
-      if (i + 1 < to) load(here, a.v, v_off, lds + (3 - odd) * L::TILE);
-      clean(i, odd, none);
-      products(1 - odd);
-    };
-    for (int i = from; i < to; i += 2) {
-      step(i, 0);
-      if (i + 1 >= to) break;
-      step(i + 1, 1);
+      load(at[1], a.k, k_off, lds + L::TILE);
+      v16f sc[2][KT];
+      v8bf wt[2][KT][2] = {};
+#pragma unroll
+      for (int x = 0; x < KT; ++x) sc[0][x] = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n) sc[0][n % KT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_k(0, n), q[n / KT], sc[0][n % KT], 0, 0, 0);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) settle(o[d]);
+      // Block i, whose buffers are `odd`.
+      auto step = [&](int i, int odd) {
+        wait_vm0();
+        lds_barrier();
+        const Where keys = at[2], values = at[0];
+        if (i > from) clean(i - 1, 1 - odd, last);
+        mask(sc[odd], i, at[0].none);
+        v8bf kf[AHEAD], vf[AHEAD];
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) {
+          kf[n] = read_k(1 - odd, n);
+          vf[n] = read_v(1 - odd, n);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        last = at[0].none;
+        at[0] = at[1];
+        at[1] = at[2];
+        at[2] = where(i + 3, ids);
+        ids = pages(i + 4);
+#pragma unroll
+        for (int x = 0; x < KT; ++x) sc[1 - odd][x] = 0.0f;
+        // of the N pairs of products, the first T come with the maximum, the next 16 KT / 2 with two weights each
+        constexpr int T = 4 * KT;
+        static_assert(T + 1 + 8 * KT <= N && 4 * L::LOADS == N, "a place for each");
+        float tops[2] = {mx, mx}, old = mx, alpha = 1.0f, sums[2];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          __builtin_amdgcn_sched_barrier(0);
+          sc[1 - odd][n % KT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[n % AHEAD], q[n / KT], sc[1 - odd][n % KT], 0, 0, 0);
+          // what one product hides comes behind each of the two
+          if (n + AHEAD < N) kf[n % AHEAD] = read_k(1 - odd, n + AHEAD);
+          const int x = n < T ? n / 4 : n <= T + 8 * KT ? (n - T - 1) / 8 : 0, r = n < T ? n % 4 * 4 : (n - T - 1) % 8 * 2;
+          const v16f& now = sc[odd][x];
+          v2bf pair;
+          if (n < T) {
+            tops[0] = fmaxf(fmaxf(tops[0], now[r]), now[r + 1]);
+            tops[1] = fmaxf(fmaxf(tops[1], now[r + 2]), now[r + 3]);
+          } else if (n == T) {
+            const float top = max_halves(fmaxf(tops[0], tops[1]));
+            mx = (top - mx) * scale > 8.0f ? top : mx;
+          } else if (n <= T + 8 * KT) {
+            pair[0] = static_cast<__bf16>(__builtin_amdgcn_exp2f((now[r] - mx) * scale));
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          add_values(o[n % DT], vf[n % AHEAD], wt[1 - odd][n / (2 * DT)][n / DT % 2]);
+          if (n + AHEAD < N) vf[n % AHEAD] = read_v(1 - odd, n + AHEAD);
+          // loads among the products: in one go behind the barrier they would keep the waves from them while the
+          // address unit takes them (the last blocks' keys once more where there are no further)
+          if (n % 4 == 1)
+            load_one(values, a.v, v_off, lds + (2 + odd) * L::TILE, n / 4);
+          else if (n % 4 == 3)
+            load_one(keys, a.k, k_off, lds + odd * L::TILE, n / 4);
+          if (n == T) {
+            alpha = __builtin_amdgcn_exp2f((old - mx) * scale);
+            sums[0] = sum * alpha;
+            sums[1] = 0.0f;
+          } else if (n > T && n <= T + 8 * KT) {
+            pair[1] = static_cast<__bf16>(__builtin_amdgcn_exp2f((now[r + 1] - mx) * scale));
+            asm volatile("" : "+v"(pair));  // formed here, not behind the products
+            sums[n & 1] = add_pair(pair, sums[n & 1]);
+            wt[odd][x][r >> 3][r & 7] = pair[0];
+            wt[odd][x][r >> 3][(r & 7) + 1] = pair[1];
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        sum = sums[0] + sums[1];
+        if (i > from && __any(mx != old)) {  // (before the first there is nothing)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            settle(o[d]);
+            o[d] *= alpha;
+            settle(o[d]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      };
+      auto finish = [&](int odd) {  // the last block's values
+        wait_vm0();
+        lds_barrier();
+        clean(to - 1, odd, last);
+#pragma unroll
+        for (int n = 0; n < N; ++n) add_values(o[n % DT], read_v(odd, n), wt[odd][n / (2 * DT)][n / DT % 2]);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) settle(o[d]);
+      };
+      int i = from;
+      for (; i + 1 < to; i += 2) {
+        step(i, 0);
+        step(i + 1, 1);
+      }
+      if (i < to) {
+        step(i, 0);
+        finish(0);
+      } else {
+        finish(1);
+      }
+    } else {
+      // here: block i's keys, then: block i + 1's, ids: the pages of block i + 2
+      Where here = where(from, pages(from)), then = where(from + 1, pages(from + 1));
+      int ids = pages(from + 2);
+      load(here, a.k, k_off, lds);
+      wait_vm0();
+      bare_barrier();
+      load(then, a.k, k_off, lds + L::TILE);  // the last block once more where there is none
+      load(here, a.v, v_off, lds + 2 * L::TILE);
+#pragma unroll
+      for (int x = 0; x < KT; ++x) s[x] = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n) s[n % KT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_k(0, n), q[n / KT], s[n % KT], 0, 0, 0);
+      // Block i, whose buffers are `odd`: its weights, then its second product beside the next one's scores
+      // (of the last, what the buffer holds: they are not used).
+      auto step = [&](int i, int odd) {
+        weigh(i, here.none);
+        wait_vm0();
+        lds_barrier();
+        const uint64_t none = here.none;
+        here = then;
+        then = where(i + 2, ids);
+        ids = pages(i + 3);
+        if (i + 2 < to) load(then, a.k, k_off, lds + odd * L::TILE);
+        if (i + 1 < to) load(here, a.v, v_off, lds + (3 - odd) * L::TILE);
+        clean(i, odd, none);
+        products(1 - odd);
+      };
+      for (int i = from; i < to; i += 2) {
+        step(i, 0);
+        if (i + 1 >= to) break;
+        step(i + 1, 1);
+      }
+      wait_vm0();
     }
-    wait_vm0();
   }
 
-  sum += other_half(sum);
+  sum = add_halves(sum);
   const bool whole = splits == 1;
   const float inv = !whole ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
-  if (first_row + l32 >= rows) return;
-  // registers 4 r .. 4 r + 3 of O^T: elements d * 32 + 8 r + 4 half .. + 3 of the lane's row
+  // Out through the wave's quarter of LDS, so that stores are whole rows: registers 4 r .. 4 r + 3 of O^T are
+  // elements d * 32 + 8 r + 4 half .. + 3 of the lane's row, which alone would be 16 bytes of 32 rows a store.
+  bare_barrier();  // the buffers are free
+  char* mem = smem + wave * L::TILE;
+  auto leave = [&](auto* to, auto type) {
+    typedef decltype(type) piece;                                   // four elements
+    constexpr int ROWB = D / 4 * sizeof(piece), CH = ROWB / 16, TURN = CH < 16 ? CH - 1 : 15;
+    static_assert(32 * ROWB <= L::TILE, "a quarter holds the wave's rows");
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      const v4f v = v4f{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]} * inv;
-      const int64_t at = d * 32 + 2 * r + 4 * half;
-      if (whole)
-        *reinterpret_cast<v4bf*>(a.out + out_row * D + at) = __builtin_convertvector(v, v4bf);
-      else
-        *reinterpret_cast<v4f*>(a.part + (static_cast<int64_t>(split) * a.T * a.n_q + out_row) * D + at) = v;
+      for (int r = 0; r < 16; r += 4) {
+        const v4f v = v4f{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]} * inv;
+        const int byte = (d * 8 + r / 2 + half) * static_cast<int>(sizeof(piece));
+        *reinterpret_cast<piece*>(mem + l32 * ROWB + ((byte / 16) ^ (l32 & TURN)) * 16 + byte % 16) = __builtin_convertvector(v, piece);
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 32 * CH / 64; ++j) {
+      const int r = (j * 64 + lane) / CH, c = lane % CH;
+      const v4f v = *reinterpret_cast<const v4f*>(mem + r * ROWB + (c ^ (r & TURN)) * 16);
+      const int64_t at = static_cast<int64_t>(__shfl(static_cast<int>(out_row), r)) * ROWB + c * 16;
+      if (first_row + r < rows) *reinterpret_cast<v4f*>(reinterpret_cast<char*>(to) + at) = v;
     }
-  if (!whole && half == 0) {
-    float* ml = a.part + static_cast<int64_t>(a.max_splits) * a.T * a.n_q * D + (static_cast<int64_t>(split) * a.T * a.n_q + out_row) * 2;
+  };
+  if (whole) {
+    leave(a.out, v4bf());
+    return;
+  }
+  const int64_t plane = static_cast<int64_t>(a.T) * a.n_q;
+  leave(a.part + split * plane * D, v4f());
+  if (half == 0 && first_row + l32 < rows) {
+    float* ml = a.part + a.max_splits * plane * D + (split * plane + out_row) * 2;
     ml[0] = mx * scale;
     ml[1] = sum;
   }
@@ -712,7 +880,7 @@ Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_k
     const int64_t keys = window == 0 ? table_keys : std::min<int64_t>(table_keys, static_cast<int64_t>(window) + sinks + rows / group + 1 + 2 * size);
     return (keys + size - 1) / size * size;
   };
-  const int64_t keys = reach(kSmallRows, kSmallKeys), large_size = D < 256 ? 64 : 32;
+  const int64_t keys = reach(kSmallRows, kSmallKeys);
   // Few rows: workgroups that share a tile's keys, enough to fill the device (several times over, for lengths
   // that differ: 24 tokens of up to 16384 keys of 256 took 227 us with one workgroup a CU, 203 with two, 188 with
   // four, 199 with eight) and none of less than kSplitBlocks blocks of what the table can hold.
@@ -725,7 +893,7 @@ Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_k
   // kernel and the sums' way through memory (4 TB/s).  us with the splits chosen and without: 512 of 16384 keys
   // 185 and 387, 2 x 924 tokens of 4 heads 25 and 33; 512 tokens of 40 heads 22 without, 33 with 3.
   const int64_t large_tiles = std::max<int64_t>(1, T * group * n_kv / 128), places = (D < 256 ? 2 : 1) * dev.cu_count;
-  const int64_t blocks = reach(128, static_cast<int>(large_size)) / large_size;
+  const int64_t blocks = reach(128, 64) / 64;
   float large_us = 0.0f;
   for (int64_t n = 1; n == 1 || (n <= std::min<int64_t>(kMostSplits, blocks / kLargeSplitBlocks) && n * large_tiles <= places); ++n) {
     float us = 1.7f * static_cast<float>((blocks + n - 1) / n) * static_cast<float>((n * large_tiles + places - 1) / places);

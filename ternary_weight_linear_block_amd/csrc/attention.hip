@@ -369,7 +369,7 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
 // of 64 and 128: two or three workgroups share a CU, so that one has its products while another has its
 // exponentials; 8192 tokens of 40 heads of 128, window 4096: 510 us, 1010 TFLOP/s (the library's product of
 // 8192^3 in bf16: 1399).  Heads of 256 (O takes 128 registers): one, with all of it between a wave's own
-// products; 4096 causal tokens of 20 heads 210 us, 820 TFLOP/s (one after the other: 243).  What a tile costs
+// products; 4096 causal tokens of 20 heads 215 us, 800 TFLOP/s (one after the other: 243).  What a tile costs
 // beside its blocks, 12 us with two on a CU and 17 alone, is a chain of waits: its sequence, pages, first keys, stores.
 template <int D>
 struct Large {
@@ -492,13 +492,15 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
     const v4bf lo = read_tr(at), hi = read_tr(at + 8 * ROW);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  // O of a wave alone on its SIMD lies in accumulation registers, 128 beside the 200 of all else, which the
-  // compiler does not do by itself (it moved parts of it to and fro, 298 us for 4096 tokens).  It does not
-  // know what the instruction needs either: two states between a weight's last operation and its use, and
-  // `settle` before and behind other operations on O.
+  // O of a wave alone on its SIMD lies in accumulation registers, 128 beside the 240 of all else, which the
+  // compiler does not do by itself (it moved parts of it to and fro, 298 us for 4096 tokens).  It does not know
+  // what the instruction is either.  Its operands come from LDS loads, for which the compiler waits, and from
+  // before a barrier; 19 states must pass between the instruction and another's use of O: `drain` behind the last
+  // product of a block, `settle` around other operations on O.
   auto add_values = [&](v16f& acc, v8bf v, v8bf p) {
     asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(v), "v"(p));
   };
+  auto drain = [] { asm volatile("s_nop 15\n\ts_nop 3" ::: "memory"); };
   auto settle = [](v16f& acc) { asm volatile("s_nop 15\n\ts_nop 15" : "+a"(acc)); };
   // The scores of the block in buffer `odd` and the second product of the one before it, in turn
   // (their chains of products are apart), operands read AHEAD products before.
@@ -689,6 +691,8 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
           }
         }
         __builtin_amdgcn_sched_barrier(0);
+        drain();  // copies of O that the compiler makes on its way out of here find it whole
+        __builtin_amdgcn_sched_barrier(0);
         sum = sums[0] + sums[1];
         if (i > from && __any(mx != old)) {  // (before the first there is nothing)
 #pragma unroll
@@ -706,6 +710,7 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
         clean(to - 1, odd, last);
 #pragma unroll
         for (int n = 0; n < N; ++n) add_values(o[n % DT], read_v(odd, n), wt[odd][n / (2 * DT)][n / DT % 2]);
+        drain();
 #pragma unroll
         for (int d = 0; d < DT; ++d) settle(o[d]);
       };

@@ -63,6 +63,14 @@ struct Tile {
   int seen;           // keys that the page table holds, at most kv
 };
 
+__device__ __forceinline__ void set_sequence(const AttnArgs& a, int seq, int start, int end, int kv, Tile* t) {
+  t->seq = seq;
+  t->q0 = min(max(start, 0), a.T);
+  t->n = min(max(end, t->q0), a.T) - t->q0;
+  t->kv = min(max(kv, 0), kMostKeys);
+  t->seen = a.n_pages > 0 ? static_cast<int>(min(static_cast<int64_t>(t->kv), static_cast<int64_t>(a.table_pages) << a.page_shift)) : 0;
+}
+
 // The last sequence whose start, scaled by `before(start, b)`, is not beyond what is looked
 // for: each lane looks at one sequence, and what the found one needs comes with it.
 template <class Before>
@@ -75,14 +83,11 @@ __device__ __forceinline__ bool find_sequence(const AttnArgs& a, int lane, Tile*
     const int here = __popcll(__ballot(base + lane < a.B && before(q0, b)));
     if (here > 0) {
       found = true;
-      t->seq = base + here - 1;
-      t->q0 = __builtin_amdgcn_readlane(q0, here - 1);
-      t->n = min(max(__builtin_amdgcn_readlane(end, here - 1), t->q0), a.T) - t->q0;
-      t->kv = min(max(__builtin_amdgcn_readlane(kv, here - 1), 0), kMostKeys);
+      set_sequence(a, base + here - 1, __builtin_amdgcn_readlane(start, here - 1), __builtin_amdgcn_readlane(end, here - 1),
+                   __builtin_amdgcn_readlane(kv, here - 1), t);
     }
     if (here < 64) break;
   }
-  t->seen = a.n_pages > 0 ? static_cast<int>(min(static_cast<int64_t>(t->kv), static_cast<int64_t>(a.table_pages) << a.page_shift)) : 0;
   return found;
 }
 
@@ -117,6 +122,11 @@ __device__ __forceinline__ Blocks find_blocks(const AttnArgs& a, const Tile& t, 
 // Splits of a tile's blocks that do work: at most a.splits, each of kSplitBlocks or more.
 constexpr int kSmallRows = 16, kSmallKeys = 32, kSmallWaves = 4, kSplitBlocks = 2 * kSmallWaves;
 constexpr int kLargeSplitBlocks = 2;
+
+// Sequences of more packed rows than this take the kernel for many rows (where the call may hold any); the
+// kernel for few rows then has kShortTiles tiles for each sequence.
+constexpr int kSmallMost = 64, kShortTiles = kSmallMost / kSmallRows;
+constexpr int kAllRows = 1 << 30;  // small_rows where the kernel for few rows takes all sequences
 
 __device__ __forceinline__ int large_splits(const AttnArgs& a, int total) {
   return max(1, min(a.large_splits, total / kLargeSplitBlocks));
@@ -176,7 +186,15 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
   const int head = blockIdx.x % a.n_kv;
   const int split = blockIdx.x / a.n_kv % a.splits;
   Tile t;
-  if (!find_tile(a, blockIdx.x / a.n_kv / a.splits, kSmallRows, lane, &t) || t.n * a.group > a.small_rows) return;
+  const int tile = blockIdx.x / a.n_kv / a.splits;
+  if (a.small_rows == kAllRows) {
+    if (!find_tile(a, tile, kSmallRows, lane, &t)) return;
+  } else {
+    const int b = tile / kShortTiles;
+    set_sequence(a, b, a.q_start[b], a.q_start[b + 1], a.kv_len[b], &t);
+    t.row0 = tile % kShortTiles * kSmallRows;
+    if (t.row0 >= t.n * a.group || t.n * a.group > a.small_rows) return;
+  }
   const Blocks k = find_blocks(a, t, kSmallRows, kSmallKeys);
   const int splits = active_splits(a, k.total);
   if (split >= splits) return;
@@ -867,9 +885,6 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 
 int64_t tiles_of(const AttnArgs& a, int rows) { return static_cast<int64_t>(a.T) * a.group / rows + a.B; }
 
-// Sequences of more packed rows than this take the kernel for many rows (where the call may hold any).
-constexpr int kSmallMost = 64;
-
 // What a call launches.  The lengths are on the device: a call of few rows for its sequences
 // runs the kernel for few rows alone, whatever the lengths; others run both, and each
 // sequence's length says which one takes it.
@@ -916,7 +931,7 @@ Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_k
   const bool few = T * group <= kSmallMost * B || small_us < large_us + (B > 1 ? 4.0f : 0.0f);
   p.small = few || B > 1;
   p.large = !few;
-  p.small_rows = few ? 1 << 30 : B == 1 ? 0 : kSmallMost;
+  p.small_rows = few ? kAllRows : B == 1 ? 0 : kSmallMost;
   if (!p.small) p.splits = 1;
   if (!p.large) p.large_splits = 1;
   p.max_splits = std::max(p.splits, p.large_splits);
@@ -933,8 +948,10 @@ hipError_t launch_d(AttnArgs a, const Plan& p, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const uint32_t tiles = static_cast<uint32_t>(tiles_of(a, kSmallRows)) * a.n_kv;
   if (p.small) {
+    // beside the other kernel, tiles by sequence: those of all rows, nearly all without work, took 7 us of
+    // five chunks' 107
+    const uint32_t tiles = static_cast<uint32_t>(p.large ? static_cast<int64_t>(a.B) * kShortTiles : tiles_of(a, kSmallRows)) * a.n_kv;
     attention_small_kernel<D><<<tiles * a.splits, 256, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -174,6 +174,11 @@ __device__ __forceinline__ int active_splits(const AttnArgs& a, int total) {
 // S^T = K Q^T on 16x16x32 MFMAs: a lane holds row lane % 16 and, with the rows of K
 // taken in the order below, the scores of keys 8 (lane / 16) .. + 7 of a block, which
 // is where O^T = V^T P^T wants its P.  V^T comes from the wave's own LDS by transposing reads.
+//
+// Bound by the stream of keys and values: 24 tokens of up to 16384 keys of 256, 924 MB, 187 us, 4.9 TB/s, 96%
+// of a copy; short contexts by a chain of trips to memory (lengths, pages, keys), 6 us and the join's 4.  A wave's
+// next block is in flight, keys to registers and values to LDS, while it works on one (before, 232 us); waves
+// take blocks of their own, so that no barrier stands between the loads and the end.
 template <int D>
 __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
   constexpr int C = D / 32;                 // steps of 32 along D

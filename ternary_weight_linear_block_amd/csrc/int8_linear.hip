@@ -12,8 +12,8 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-constexpr int kGroup = 8;       // rows of tiles in an XCD's order
-constexpr int kXcds = 8;      // workgroups are dispatched to the XCDs round robin
+constexpr int kGroup = 8;  // rows of tiles in an XCD's order
+constexpr int kXcds = 8;   // workgroups are dispatched to the XCDs round robin
 
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
@@ -120,7 +120,13 @@ __device__ __forceinline__ void store_rows(void* out, int M, int N, int row0, in
 // ---------------------------------------------------------------------------------
 // Few tokens: 16 RT rows of w and 16 MT tokens a workgroup, whose waves share K.  The
 // weights go from memory into MFMA operands as they lie: a lane loads 16 bytes of row
-// lane % 16, four lanes 64 bytes of a row; U steps of 64 bytes are in flight in a wave.
+// lane % 16; U steps of 128 bytes of each row are in flight in a wave.
+//
+// Bound by the stream of w (at M <= 32 each byte is used by at most 64 operations, a sixth of what
+// the MFMAs do in its time): no LDS, no barrier before the end, only loads that are
+// deep enough.  1 token 5120 -> 7168 9.6 us (3.8 TB/s; too short to reach the rate of a copy, 5.1), 24 tokens
+// 5120 -> 65536 73 us (4.6 TB/s).  Whole cache lines by four lanes instead of half ones: 24 tokens
+// 17408 -> 5120 44 -> 32 us.
 
 template <int RT, int MT, int WAVES, int U, int KIND>
 __global__ __launch_bounds__(64 * WAVES) void int8_rows_kernel(Int8Args a) {
@@ -197,7 +203,13 @@ __global__ __launch_bounds__(64 * WAVES) void int8_rows_kernel(Int8Args a) {
 }
 
 // ---------------------------------------------------------------------------------
-// Many tokens: a tile of BM tokens x BN channels a workgroup of WM x WN waves.
+// Many tokens: a tile of BM tokens x BN channels a workgroup of WM x WN waves, on 32x32x32 MFMAs; stages of
+// 128 of K go to LDS by direct loads, STAGES of them in flight.
+//
+// Bound by the MFMAs: 4096 tokens 5120 -> 17408 349 us, 2.09 POP/s, 8192^3 467 us, 2.35 (the library's product
+// of that size 2.15).  To get there from 392 us: loads of a stage issued one by one among its products, not in
+// one go; a stage's buffer handed on as soon as its last operands are in registers; operands read a
+// step ahead, across the barrier.  Without gain: a prefetch of w into L2, stages of 64, four waves of 64 x 64.
 
 template <int BM_, int BN_, int WM_, int WN_, int SK_, int STAGES_>
 struct Tile {
@@ -461,7 +473,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
     return p;
   }
   // The plan of least time: rounds of workgroups by the table, a second kernel and the
-  // sums' traffic (4 TB/s) where K is split.  24 tokens and up never split below 4 stages.
+  // sums' traffic (4 TB/s) where K is split, into parts of at least 4 stages.
   const int64_t stages = (K + 127) / 128;
   float best = 0.0f;
   for (int t = 0; t < 6; ++t) {

@@ -1,8 +1,8 @@
 """qk_norm_rope on the GPU against the float64 oracle, element by element.
 
 The bound.  u = 2^-24.  The sum of D squares in fp32 is off by at most the roundings of a
-chain: 8 in a lane and up to 5 exchanges, 13 u; the mean, eps, square root and quotient
-add 4 u, half of the sum's error passes the root: n = x r w is within 13/2 + 4 + 2 < 13 u of
+chain: 8 in a lane and up to 5 exchanges, 13 u; the mean and eps add 2 u, half of that passes
+the reciprocal root, which adds 2 u (1 ulp): n = x r w is within 15/2 + 2 + 2 < 13 u of
 its value.  A turned element adds two products: within (13 + 2) u of |a c| + |b s|.  One
 rounding to bf16: 2^-8 of the result.  Products below bf16's smallest normal number round by
 at most 2^-134."""

@@ -167,3 +167,42 @@ def test_two_streams_at_once(twl):
     for i in range(2):
         assert all(torch.equal(t, want[i]) for t in got[i])
         assert all(torch.equal(t, want_i[i]) for t in got_i[i])
+
+
+@pytest.mark.parametrize("M,N,K", [(150, 2 ** 24 - 3, 32), (200, 2 ** 24, 16)])
+def test_int8_outputs_past_32_bits(twl, M, N, K):
+    announce(f"int8_linear {M} x {K} -> {N}")
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    w = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    out = twl.int8_linear(x, None, w, None, out_dtype=torch.int32)
+    for n in (0, N // 2 - 500, N - 1000):
+        assert torch.equal(out[:, n:n + 1000], (x.double() @ w[n:n + 1000].double().T).int())
+    assert torch.equal(out[M - 1], (w.float() * x[M - 1].float()).sum(1).int())  # sums below 2^24: exact in fp32
+
+
+def test_rope_rows_past_32_bits(twl):
+    M, n_q, n_kv, D = 600_000, 14, 1, 256
+    announce(f"qk_norm_rope {M} tokens")
+    qkv = torch.randn(M, (n_q + 2 * n_kv) * D, dtype=torch.bfloat16, device="cuda")
+    positions = torch.arange(M, dtype=torch.int32, device="cuda") % N_POS
+    cos_sin, w = dev(test_gpu_rope._table(N_POS, D)), torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    got = twl.qk_norm_rope(qkv, positions, cos_sin, n_q, n_kv, q_weight=w, k_weight=w)
+    for rows in (slice(0, 100), slice(M - 300_000, M - 299_900), slice(M - 100, M)):
+        alone = twl.qk_norm_rope(qkv[rows], positions[rows].clone(), cos_sin, n_q, n_kv, q_weight=w, k_weight=w)
+        assert all(torch.equal(a[rows], b) for a, b in zip(got, alone))
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_attention_rows_past_32_bits(twl, D):
+    T, n_q, page = 2 ** 25 // D, 64, 64
+    T += 1000
+    announce(f"window_attention {T} tokens of {n_q} heads of {D}")
+    q = torch.randn(T, n_q, D, dtype=torch.bfloat16, device="cuda")
+    pages = -(-T // page)
+    k = torch.randn(pages, 1, page, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.randn(pages, 1, page, D, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    out = twl.window_attention(q, k, v, table, dev(np.array([0, T], np.int32)), dev(np.array([T], np.int32)), window=1)
+    want = v.view(-1, D)[:T]  # each row sees its own key alone
+    assert all(torch.equal(out[:, h], want) for h in range(n_q))

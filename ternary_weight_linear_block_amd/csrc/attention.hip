@@ -916,7 +916,7 @@ Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_k
   // Many rows: where the tiles leave workgroups' places free (two a CU, one for D = 256), splits, if what
   // they save (a block of keys takes 1.7 us where few workgroups run) is more than the second
   // kernel and the sums' way through memory (4 TB/s).  us with the splits chosen and without: 512 of 16384 keys
-  // 185 and 387, 2 x 924 tokens of 4 heads 25 and 33; 512 tokens of 40 heads 22 without, 33 with 3.
+  // 185 and 333, 200 of 4000 43 and 91, 2 x 2430 tokens of 2 heads of 64 36 and 45; 512 tokens of 40 heads 19 without, 35 with 3.
   const int64_t large_tiles = std::max<int64_t>(1, T * group * n_kv / 128), places = (D < 256 ? 2 : 1) * dev.cu_count;
   const int64_t blocks = reach(128, 64) / 64;
   float large_us = 0.0f;
@@ -929,8 +929,8 @@ Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_k
   }
   // Which of the two: the kernel for few rows reads a tile's keys for 16 rows instead of 128 (25000 keys a us
   // for all tiles of D = 128), but has its keys shared by four waves and needs no second launch in a batch.
-  // us, few and many: 2 x 28 tokens of 56 keys of 256 10.5 and 20, 10 x 111 of 223 10.3 and 20; 200 tokens of 4000
-  // keys 86 and 43.  A round of workgroups that waits for places (four a CU, two, one by D) adds 4 us.
+  // us, few and many: 2 x 28 tokens of 56 keys of 256 8 and 20, 10 x 111 of 223 10 and 18; 200 tokens of 4000
+  // keys 87 and 43, 512 causal tokens 26 and 19.  A round of workgroups that waits for places (four a CU, two, one by D) adds 4 us.
   const float small_us = std::max(static_cast<float>(tiles * keys) * static_cast<float>(D) / 128.0f / 25000.0f, static_cast<float>(keys) * 0.01f / static_cast<float>(p.splits)) +
                          (p.splits > 1 ? 4.0f : 0.0f) + 4.0f * static_cast<float>(tiles * p.splits / ((D == 64 ? 4 : D == 128 ? 2 : 1) * dev.cu_count));
   const bool few = T * group <= kSmallMost * B || small_us < large_us + (B > 1 ? 4.0f : 0.0f);

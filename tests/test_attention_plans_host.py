@@ -8,6 +8,7 @@ import subprocess
 import pytest
 
 pytest.importorskip("torch")
+from tests import test_gpu_attention_large as L  # noqa: E402
 from tests import test_gpu_int8_tiles as I  # noqa: E402
 from tests.test_host_sanitized import CSRC, ROOT, _hipcc  # noqa: E402
 
@@ -34,6 +35,39 @@ def plans(tmp_path_factory):
         assert len(out) == len(sizes)
         return out
     return ask
+
+
+def _attention_sizes(lengths, shape, split, window, sinks):
+    """T, B, group, n_kv, D, the table's keys, window and sinks of test_gpu_attention_large.case."""
+    D, n_q, n_kv, page = shape
+    rows, keys = L.form(D, split)
+    pages = max(1, keys // page, *(-(-kv // page) for _, kv in lengths))
+    return max(sum(n for n, _ in lengths), -(-rows // n_q)), len(lengths), n_q // n_kv, n_kv, D, pages * page, window, sinks
+
+
+def test_attention_calls_take_the_kernel_for_many_rows(plans):
+    calls = list(L.calls())
+    got = plans("attention", [_attention_sizes(*c[:5]) for c in calls])
+    reached = set()
+    for call, (small, large, small_rows, _, large_splits) in zip(calls, got):
+        assert large and (large_splits > 1) == call[5], (call, large, large_splits)
+        assert small == (len(call[0]) > 1) and small_rows == (64 if small else 0)  # which rows the other kernel takes
+        reached.add((call[1][0], small, min(large_splits, 3)))
+    assert reached == {(D, small, splits) for D in (64, 128, 256) for small in (0, 1) for splits in (1, 2, 3)}
+
+
+def test_sizes_of_the_calls(plans):
+    """_attention_sizes gives what the cases hold."""
+    for lengths, shape, split in ((L.BESIDE[0], L.SHAPES[1], False), (L.LONG[1], L.SHAPES[4], True), (L.EMPTY, L.ONE[64], False)):
+        try:
+            made = {}
+            keep, L.S._case = L.S._case, lambda *a, **kw: made.update(a=a, kw=kw)
+            L.case(0, lengths, shape, split)
+        finally:
+            L.S._case = keep
+        page, need = made["a"][5], max([-(-kv // made["a"][5]) for _, kv in lengths] + [1])
+        T, _, _, _, _, keys, _, _ = _attention_sizes(lengths, shape, split, 0, 0)
+        assert (sum(n for n, _ in lengths) + made["kw"]["spare_rows"], (need + made["kw"]["wide"]) * page) == (T, keys)
 
 
 def test_int8_sizes_take_the_kernel_they_name(plans):

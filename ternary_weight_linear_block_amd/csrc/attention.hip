@@ -518,10 +518,15 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
   // O of a wave alone on its SIMD lies in accumulation registers, 128 beside the 240 of all else, which the
   // compiler does not do by itself (it moved parts of it to and fro, 298 us for 4096 tokens).  It does not know
   // what the instruction is either.  Its operands come from LDS loads, for which the compiler waits, and from
-  // before a barrier; 19 states must pass between the instruction and another's use of O: `drain` behind the last
-  // product of a block, `settle` around other operations on O.
+  // before a barrier.  12 states must pass between the instruction and another's use of O: `drain` (20) behind the
+  // last product of a block, `settle` around other operations on O.  Two must pass between an operation that writes O
+  // and the instruction: add_last has them, since the compiler copies O right before the last block's products.
+  // The build checks the distances in what the compiler made (codegen.py).
   auto add_values = [&](v16f& acc, v8bf v, v8bf p) {
     asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(v), "v"(p));
+  };
+  auto add_last = [&](v16f& acc, v8bf v, v8bf p) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(v), "v"(p));
   };
   auto drain = [] { asm volatile("s_nop 15\n\ts_nop 3" ::: "memory"); };
   auto settle = [](v16f& acc) { asm volatile("s_nop 15\n\ts_nop 15" : "+a"(acc)); };
@@ -732,7 +737,7 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
         lds_barrier();
         clean(to - 1, odd, last);
 #pragma unroll
-        for (int n = 0; n < N; ++n) add_values(o[n % DT], read_v(odd, n), wt[odd][n / (2 * DT)][n / DT % 2]);
+        for (int n = 0; n < N; ++n) add_last(o[n % DT], read_v(odd, n), wt[odd][n / (2 * DT)][n / DT % 2]);
         drain();
 #pragma unroll
         for (int d = 0; d < DT; ++d) settle(o[d]);

@@ -5,7 +5,9 @@
 Every HIP source is compiled with -O3 for gfx950 only, without fast-math
 (the rotation depends on IEEE fp32 adds, correctly rounded division and
 ties-to-even rint), with floating-point contraction off and packed-fp32
-instruction selection disabled.
+instruction selection disabled.  Where a source has instructions written out, the
+assembly that its object is made of is checked (codegen.py); a distance that another
+compiler made too short ends the build.
 """
 from __future__ import annotations
 
@@ -15,6 +17,9 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+
+from . import codegen
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -30,6 +35,9 @@ PEAKS_LIB_PATH = os.path.join(PKG_DIR, "libtwl_peaks.so")
 SOURCES = ["rotate_quant.hip", "pack.hip", "gemm_i8.hip", "gemv.hip", "gemv_gated.hip", "reference_bf16.hip",
            "norm_rotate.hip", "lora.hip", "int8_linear.hip", "qk_rope.hip", "attention.hip", "api.cpp", "api_block.cpp",
            "api_attention.cpp"]
+
+# sources with matrix products or loads to LDS in inline assembly
+CHECKED = ["gemm_i8.hip", "gemv.hip", "gemv_gated.hip", "int8_linear.hip", "attention.hip"]
 
 ARCH = "gfx950"
 COMMON_FLAGS = [
@@ -59,17 +67,29 @@ def hipcc() -> str:
 
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [hipcc()] + COMMON_FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
-    if src.endswith(".cpp"):
-        cmd[1:1] = ["-x", "hip"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    out = "\n".join(ln for ln in (res.stdout + res.stderr).splitlines()
-                    if "unknown target feature" not in ln and "packed-fp32-ops" not in ln
-                    and ln.strip())
-    if res.returncode != 0:
-        raise RuntimeError(f"compiling {src} failed:\n{out}")
+    with tempfile.TemporaryDirectory(dir=BUILD_DIR) as tmp:
+        made = os.path.join(tmp, os.path.basename(obj))
+        cmd = [hipcc()] + COMMON_FLAGS + ["-c", os.path.join(CSRC, src), "-o", made]
+        if src.endswith(".cpp"):
+            cmd[1:1] = ["-x", "hip"]
+        if src in CHECKED:
+            cmd.insert(1, "-save-temps=obj")
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        out = "\n".join(ln for ln in (res.stdout + res.stderr).splitlines()
+                        if "unknown target feature" not in ln and "packed-fp32-ops" not in ln
+                        and ln.strip())
+        if res.returncode != 0:
+            raise RuntimeError(f"compiling {src} failed:\n{out}")
+        if src in CHECKED:
+            asm = [f for f in os.listdir(tmp) if f.endswith(".s") and ARCH in f]
+            if len(asm) != 1:
+                raise RuntimeError(f"{src}: the compiler left {len(asm)} assembly files of {ARCH}")
+            with open(os.path.join(tmp, asm[0])) as f:
+                if not any(codegen.check(f.read())):
+                    raise RuntimeError(f"{src}: its written-out instructions are not in the generated code")
+        os.replace(made, obj)
     if verbose and out:
         print(out)
     return obj

@@ -1,11 +1,14 @@
 """The distances that written-out instructions need in the generated gfx950 code (the package's
 codegen.py, which the build runs): on the library's sources, on code with a distance taken
 away, and on short texts for each rule, through branches and around loops."""
+import os
 import re
+import shutil
 
 import pytest
 
 from tests.test_codegen_host import _compile_asm
+from ternary_weight_linear_block_amd import build as B
 from ternary_weight_linear_block_amd import codegen
 
 PRODUCT = "v_mfma_f32_32x32x16_bf16 a[0:15], v[0:3], v[4:7], a[0:15]"
@@ -84,3 +87,29 @@ def test_through_branches():
     assert _check(PRODUCT, "s_nop 15", "s_nop 3", *skip) == (1, 0)
     # behind an unconditional branch nothing comes from above
     assert _check(PRODUCT, "s_branch .LBB0_2", "v_accvgpr_read_b32 v9, a0", ".LBB0_2:", "s_endpgm") == (1, 0)
+
+
+def test_the_build_refuses_what_is_too_close(tmp_path, monkeypatch):
+    if not os.path.exists(shutil.which("hipcc") or "/opt/rocm/bin/hipcc"):
+        pytest.skip("hipcc not available")
+    source = tmp_path / "csrc"
+    shutil.copytree(B.CSRC, source)
+    text = (source / "attention.hip").read_text()
+    assert text.count("s_nop 1\\n\\tv_mfma") == 1
+    (source / "attention.hip").write_text(text.replace("s_nop 1\\n\\tv_mfma", "v_mfma"))
+    (tmp_path / "out").mkdir()
+    monkeypatch.setattr(B, "CSRC", str(source))
+    monkeypatch.setattr(B, "BUILD_DIR", str(tmp_path / "out"))
+    with pytest.raises(RuntimeError, match="attention_large_kernelILi256E"):
+        B._compile("attention.hip", False)
+    assert os.listdir(tmp_path / "out") == []
+    (source / "attention.hip").write_text(text)
+    assert os.path.exists(B._compile("attention.hip", False))
+
+
+def test_sources_with_instructions_written_out_are_checked():
+    for name in B.SOURCES:
+        with open(os.path.join(B.CSRC, name)) as f:
+            text = f.read()
+        if "gemv_rows.h" in text or re.search(r'"[^"\n]*(global_load_lds|v_mfma)', text):
+            assert name in B.CHECKED

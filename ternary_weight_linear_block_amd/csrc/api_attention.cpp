@@ -35,7 +35,7 @@ int page_shift(int64_t page, int64_t least) {
   return __builtin_ctzll(static_cast<unsigned long long>(page));
 }
 
-twl_status check_pages(int64_t n_pages, int64_t page, int64_t least, int64_t n_kv, int64_t D) {
+twl_status check_pages(int64_t n_pages, int64_t page, int64_t least) {
   TWL_TRY(check_rows("n_pages", n_pages));
   if (page_shift(page, least) < 0)
     return fail(TWL_ESHAPE, "page size %lld is not a power of two from %lld to 1024", static_cast<long long>(page),
@@ -52,7 +52,7 @@ twl_status check_attention(int64_t T, int64_t B, int64_t n_q, int64_t n_kv, int6
   TWL_TRY(check_rows("B", B));
   TWL_TRY(check_rows("table_pages", table_pages));
   TWL_TRY(check_heads(n_q, n_kv, D));
-  TWL_TRY(check_pages(0, page, 16, n_kv, D));
+  TWL_TRY(check_pages(0, page, 16));
   TWL_TRY(check_rows("window", window));
   TWL_TRY(check_rows("sinks", sinks));
   if (T * n_q > (int64_t{1} << 27) || B > TWL_MAX_SEQUENCES || B * n_kv > (int64_t{1} << 22))
@@ -127,7 +127,7 @@ twl_status twl_qk_norm_rope(const void* qkv, int kind, int64_t row_stride, const
                             int64_t page, hipStream_t stream) {
   TWL_TRY(check_rows("M", M));
   TWL_TRY(check_heads(n_q, n_kv, D));
-  TWL_TRY(check_pages(n_pages, page, 1, n_kv, D));
+  TWL_TRY(check_pages(n_pages, page, 1));
   const int64_t width = (n_q + 2 * n_kv) * D;
   if (kind != TWL_OUT_F32 && kind != TWL_OUT_BF16) return fail(TWL_EINVAL, "kind %d is not fp32 or bf16", kind);
   if (row_stride < width || row_stride % 8 != 0 || row_stride > (int64_t{1} << 30))
@@ -206,7 +206,7 @@ twl_status twl_window_attention(const uint16_t* q, const uint16_t* k_cache, cons
                                 int64_t table_pages, uint16_t* out, void* workspace, size_t workspace_bytes,
                                 hipStream_t stream) {
   TWL_TRY(check_attention(T, B, n_q, n_kv, D, page, table_pages, window, sinks));
-  TWL_TRY(check_pages(n_pages, page, 16, n_kv, D));
+  TWL_TRY(check_pages(n_pages, page, 16));
   if (!std::isfinite(scale) || !std::isfinite(static_cast<float>(scale * 1.4426950408889634)))
     return fail(TWL_EINVAL, "scale=%g must be finite", scale);
   if (T == 0 || B == 0) return ok();

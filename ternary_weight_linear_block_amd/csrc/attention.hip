@@ -6,6 +6,11 @@
 // over the keys j that the query at position p sees: j <= p and (p - j < window or
 // j < sinks).  One pass: m is the running maximum, and what was summed before is
 // multiplied by 2^(m_old - m_new).
+//
+// Scores, maxima and sums are fp32.  The weights p are rounded to bf16, the type of the values that
+// they meet in the second product (what the rounding leaves would take a product of its own, half
+// as many again); the sum adds the rounded ones.  Against 64 bits outputs are off by 1.7 to 2.0e-3 of
+// their norm, where weights in fp32 leave 1.6 to 1.7e-3, the rounding of the outputs alone.
 #include "attention_internal.h"
 
 #include <algorithm>
@@ -390,10 +395,11 @@ __global__ __launch_bounds__(256) void attention_small_kernel(AttnArgs a) {
 //
 // Bound by the MFMAs and, in the shadow of which they must lie, a block's exponentials and maxima.  Heads
 // of 64 and 128: two or three workgroups share a CU, so that one has its products while another has its
-// exponentials; 8192 tokens of 40 heads of 128, window 4096: 510 us, 1010 TFLOP/s (the library's product of
-// 8192^3 in bf16: 1399).  Heads of 256 (O takes 128 registers): one, with all of it between a wave's own
-// products; 4096 causal tokens of 20 heads 215 us, 800 TFLOP/s (one after the other: 243).  What a tile costs
-// beside its blocks, 12 us with two on a CU and 17 alone, is a chain of waits: its sequence, pages, first keys, stores.
+// exponentials; 8192 tokens of 40 heads of 128, window 4096: 506 to 561 us, 0.92 to 1.02 PFLOP/s (the library's
+// product of 8192^3 in bf16: 1.40; the clock falls as the calls go on).  Heads of 256 (O takes 128 registers): one,
+// with all of it between a wave's own products; 4096 causal tokens of 20 heads 215 us, 800 TFLOP/s (one after the
+// other: 243).  What a tile costs beside its blocks, 12 us with two on a CU and 17 alone, is a chain of waits: its
+// sequence, pages, first keys, stores.
 template <int D>
 struct Large {
   static constexpr int WAVES = 4, ROWS = 32 * WAVES;
@@ -588,8 +594,10 @@ __global__ __launch_bounds__(64 * Large<D>::WAVES, D < 256 ? 2 : 1) void attenti
       for (int r = 0; r < 16; r += 2) tops[r / 2 % 4] = fmaxf(fmaxf(tops[r / 2 % 4], s[x][r]), s[x][r + 1]);
     float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     top = max_halves(top);
-    // s scale - mx scale in one operation: exact but for the rounding of mx scale, a factor of all of a row's
-    // weights that divides out, and is at most 2^2 up to 2^26; beyond it the difference comes first
+    // s scale - mx scale in one operation: exact but for the rounding of mx scale.  Of the weights under one maximum
+    // that is a common factor, which divides out; those before and after a move of the maximum differ by the two
+    // roundings, half an ulp of a scaled score each (2 in the exponent at 2^26), which is no more than a score in fp32
+    // leaves open itself.  Beyond 2^26 the difference comes first.
     float factor = scale, shift = mx * scale;
     if (__any(((top - mx) * scale > 8.0f) | (__builtin_fabsf(shift) > 0x1p26f))) {
       const float now = fmaxf(mx, top), alpha = __builtin_amdgcn_exp2f((mx - now) * scale);
@@ -897,7 +905,10 @@ int64_t tiles_of(const AttnArgs& a, int rows) { return static_cast<int64_t>(a.T)
 
 // What a call launches.  The lengths are on the device: a call of few rows for its sequences
 // runs the kernel for few rows alone, whatever the lengths; others run both, and each
-// sequence's length says which one takes it.
+// sequence's length says which one takes it.  What the sizes do not say costs time: keys
+// are counted by the table's width, rows by all of T.  So a prompt under a wide table gets splits that
+// do not pay (512 tokens 36 us, 19 under a table of 512), and single tokens beside a chunk get few splits
+// (8 of 32768 keys and a chunk of 512 tokens 432 us, apart 198 and 68).
 struct Plan {
   bool small, large;
   int small_rows, splits, large_splits, max_splits;

@@ -206,8 +206,8 @@ __global__ __launch_bounds__(64 * WAVES) void int8_rows_kernel(Int8Args a) {
 // Many tokens: a tile of BM tokens x BN channels a workgroup of WM x WN waves, on 32x32x32 MFMAs; stages of
 // 128 of K go to LDS by direct loads, STAGES of them in flight.
 //
-// Bound by the MFMAs: 4096 tokens 5120 -> 17408 349 us, 2.09 POP/s, 8192^3 467 us, 2.35 (the library's product
-// of that size 2.15).  To get there from 392 us: loads of a stage issued one by one among its products, not in
+// Bound by the MFMAs: 4096 tokens 5120 -> 17408 342 to 376 us, 1.94 to 2.13 POP/s, 8192^3 467 us, 2.35 (the library's
+// product of that size 2.15).  To get there from 392 us: loads of a stage issued one by one among its products, not in
 // one go; a stage's buffer handed on as soon as its last operands are in registers; operands read a
 // step ahead, across the barrier.  Without gain: a prefetch of w into L2, stages of 64, four waves of 64 x 64.
 

@@ -925,7 +925,10 @@ Plan make_plan(int64_t T, int64_t B, int group, int n_kv, int D, int64_t table_k
   // Few rows: workgroups that share a tile's keys, enough to fill the device (several times over, for lengths
   // that differ: 24 tokens of up to 16384 keys of 256 took 227 us with one workgroup a CU, 203 with two, 188 with
   // four, 199 with eight) and none of less than kSplitBlocks blocks of what the table can hold.
-  const int64_t tiles = std::max<int64_t>(1, std::min(T, T * group / kSmallRows + std::min(B, T))) * n_kv;
+  // Where more than 16 query heads share a key head, a token has several tiles (9 tokens of 512 heads on one of 128, 9000
+  // keys: 48 us, 155 where one was counted; 24 of 128 heads, 8192 keys 51 and 101).
+  const int64_t wide = (group + kSmallRows - 1) / kSmallRows;
+  const int64_t tiles = std::max<int64_t>(1, std::min(T * wide, T * group / kSmallRows + std::min(B, T))) * n_kv;
   const int64_t most = std::min<int64_t>(std::max<int64_t>(1, keys / kSmallKeys / kSplitBlocks),
                                          std::min<int64_t>(kMostSplits, (1 << 23) / (B * n_kv)));  // the grid stays below 2^24 workgroups
   p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (D == 64 ? 12 : D == 128 ? 8 : 4) * dev.cu_count / tiles)));

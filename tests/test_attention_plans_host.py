@@ -85,3 +85,22 @@ def test_int8_plans_that_no_size_here_reaches(plans):
     sizes = [(int(2 ** rng.uniform(0, 13)), int(2 ** rng.uniform(0, 17)), 16 * int(2 ** rng.uniform(0, 12))) for _ in range(100000)]
     for size, (rt, mt, tile, splits) in zip(sizes, plans("int8_linear", sizes)):
         assert (rt, mt) in I.ROWS if rt else (tile, splits) in I.TILED, (size, tile, splits)
+
+
+def test_splits_of_few_rows_fill_the_device_and_no_more(plans):
+    """Workgroups of the kernel for few rows: tiles of 16 rows (a token has several where more than 16 query heads
+    share a key head) times splits are at most 12, 8 or 4 a CU, by head size, or there are no splits."""
+    import random
+    rng = random.Random(1)
+    sizes = []
+    for _ in range(20000):
+        n_kv = 2 ** rng.randrange(0, 5)
+        sizes.append((int(2 ** rng.uniform(0, 9)), int(2 ** rng.uniform(0, 7)), int(2 ** rng.uniform(0, 10)) // n_kv or 1, n_kv,
+                      rng.choice([64, 128, 256]), 16 * int(2 ** rng.uniform(0, 12)), 0, 0))
+    split = 0
+    for size, (small, _, _, splits, _) in zip(sizes, plans("attention", sizes)):
+        T, _, group, n_kv, D = size[:5]
+        if small and splits > 1:
+            split += 1
+            assert splits * (T * group // 16) * n_kv <= {64: 12, 128: 8, 256: 4}[D] * 256, (size, splits)
+    assert split > 2000

@@ -51,6 +51,9 @@ def calls():
             for window, sinks in LONG_WINDOWS:
                 yield lengths, shape, True, window, sinks, True
             yield lengths, shape, 2, 0, 0, True
+    for shape in GROUPS:
+        for window, sinks in ((0, 0), (33, 5)):
+            yield GROUPED, shape, False, window, sinks, False
     for shape in ONE.values():
         for lengths in ([(n, kv)] for n, kv in SEEN):
             for window, sinks in SEEN_WINDOWS:
@@ -61,6 +64,8 @@ def calls():
                 yield lengths, shape, split, 0, 0, split
                 for window, sinks in () if split else ((20, 3), (50, 7), (100, 4), (300, 8)):
                     yield lengths, shape, split, window, sinks, False
+        yield EXTREME, shape, False, 0, 0, False
+        yield EXTREME, shape, True, 0, 0, True
         for page in PAGES:
             for window, sinks in ((0, 0), (300, 20)):
                 yield PAGED, (*shape[:3], page), False, window, sinks, False
@@ -323,3 +328,45 @@ def test_side_stream_garbage_workspace_and_repeats(twl, D):
     torch.cuda.synchronize()
     check(c, a)
     assert torch.equal(a, b)
+
+
+# groups of more query heads than a tile has rows, up to the most
+GROUPS = [(64, 1024, 1, 16), (64, 300, 2, 32), (128, 257, 1, 64), (256, 129, 1, 16), (256, 512, 1, 16)]
+GROUPED = [(9, 70), (2, 130), (0, 3), (1, 40)]
+
+
+@pytest.mark.parametrize("shape", GROUPS, ids=str)
+def test_wide_groups(twl, shape):
+    announce(f"window_attention, many rows: {GROUPED} {shape}")
+    shape = (shape[0], shape[1] // shape[2] * shape[2], *shape[2:])
+    c = case(21, GROUPED, shape, False)
+    for window, sinks in ((0, 0), (33, 5)):
+        check(c, run(twl, c, window=window, sinks=sinks), window=window, sinks=sinks)
+
+
+EXTREME = [(140, 300), (1, 200), (90, 90)]
+
+
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("D", sorted(ONE))
+def test_extreme_scales(twl, D, split, few):
+    """Scales that leave all scores alike, and such that the largest one takes all.  Queries and keys of -1, 0 and 1 have
+    exact scores: the output is the mean of the largest ones' values, its sum of n terms off by n 2^-24, rounded once."""
+    c = S._case(22, EXTREME, *ONE[D][1:3], D, ONE[D][3]) if few else case(22, EXTREME, ONE[D], split)
+    for scale in (1e-30, -1e-38, 1e-44):
+        check(c, run(twl, c, scale=scale), scale=scale)
+    sign = dict(c, q=c["q"].sign(), k_cache=c["k_cache"].sign())
+    q, k, v = S._np(sign["q"]), np.nan_to_num(S._np(sign["k_cache"])), np.nan_to_num(S._np(c["v_cache"]))
+    starts, lens, table = host(c["q_start"]), host(c["kv_len"]), host(c["page_table"])
+    for scale in (1e30, -1e30, 1e34):
+        out = S._np(run(twl, sign, scale=scale))
+        for b in range(len(lens)):
+            n, kv = starts[b + 1] - starts[b], lens[b]
+            keys, values = A.gather(k, table[b], kv)[0], A.gather(v, table[b], kv)[0]
+            for h in range(q.shape[1]):
+                g = h // (q.shape[1] // keys.shape[0])
+                score = np.where(A.mask(n, kv, 0, 0), np.sign(scale) * q[starts[b]:starts[b + 1], h] @ keys[g].T, -np.inf)
+                best = score == score.max(1, keepdims=True)
+                want, mag = (best @ x / best.sum(1, keepdims=True) for x in (values[g], np.abs(values[g])))
+                assert (np.abs(out[starts[b]:starts[b + 1], h] - want) <= mag * (kv + 64) * S.U + np.abs(want) * 2.0 ** -7).all(), (scale, b, h)
